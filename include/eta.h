@@ -431,6 +431,134 @@ ETA_API eta_status_t eta_decode_sparse_static(const eta_shape_t* shape, const et
                                               eta_stream_t stream);
 
 /*
+ * New tokens. The three calls below put tokens into the cache and attend from
+ * one or several new tokens per row; the cache layouts, pages, lengths, dtypes,
+ * status word and shape limits are those of the calls above.
+ *
+ *  - Packed tokens: the new tokens of all rows lie one after another, row b's at
+ *    cu[b] .. cu[b + 1] - 1 (cu: [B + 1] int32, device memory, non-decreasing from
+ *    a value >= 0; rows may have none). With cu == NULL every row has exactly one,
+ *    token b being row b's (n_new = B). The host count n_new bounds cu[B]; tokens
+ *    from cu[B] on belong to no row, and their outputs are left as they were.
+ *  - Lengths count the new tokens: after this call's append row b holds seq_lens[b]
+ *    tokens, and its i-th of n_b new tokens is cache position seq_lens[b] - n_b + i.
+ *    With seq_lens == NULL every row has n_tokens; otherwise n_tokens is their host
+ *    upper bound (1 <= n_tokens <= capacity).
+ *  - Device-side values are checked on the device: a row whose cu range is not
+ *    inside [0, n_new] or whose length is below n_b or above n_tokens is skipped
+ *    (nothing of it is read, its outputs stay as they were) and
+ *    ETA_ERR_INVALID_ARG is recorded in the status word. With cu == NULL a row of
+ *    length 0 is idle: skipped without an error.
+ *  - pages may be NULL (contiguous cache). A page index outside the pool is never
+ *    read or written: ETA_ERR_INVALID_ARG is recorded and what that page would
+ *    hold takes no part.
+ */
+
+/* Rotary positions: coordinate pair i of the first rot_dim coordinates turns by
+ * position * inv_freq[i]; pairs are (i, i + rot_dim / 2), or (2 i, 2 i + 1) with
+ * interleaved = 1. rot_dim is a multiple of 16 and at most head_dim; 0 rotates
+ * nothing (inv_freq may then be NULL). Coordinates from rot_dim on pass through. */
+typedef struct {
+  const float* inv_freq; /* [rot_dim / 2] fp32, device memory */
+  int32_t rot_dim;
+  int32_t interleaved;
+} eta_rope_t;
+
+/* Packed new tokens (types: q_dtype). Rows of k and v are [Hkv][d], of q [Hq][d];
+ * consecutive tokens are `stride` elements apart, so the parts of a fused
+ * projection can be passed where they lie. Pointers and strides are multiples of
+ * 16 bytes; strides at least one row. q and q_out may both be NULL. q_out
+ * ([n_new][Hq][d], contiguous) must not overlap any input. */
+typedef struct {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;
+  int64_t q_stride, k_stride, v_stride;
+  const int32_t* cu_new; /* [B + 1] or NULL: one token per row */
+  int64_t n_new;
+} eta_tokens_t;
+
+/*
+ * eta_append_kv — rotate the new tokens' queries and keys to their positions,
+ * store keys and values in the cache, and build the metadata of the blocks that
+ * became full (as eta_build_block_meta, the same bits):
+ *   x'_i = x_i cos a - x_j sin a,  x'_j = x_j cos a + x_i sin a
+ * A stored key is this value, computed in fp64, rounded once to kv_dtype (e4m3
+ * saturates at 448); values are rounded to kv_dtype; q_out is in q_dtype.
+ *   rope : rotation (rot_dim 0: none)
+ *   k, v : the caches (or pools with pages), 16-byte aligned
+ *   meta : of this shape; mu == NULL builds none. With the sub-block envelope pass
+ *          the shape whose block_size is b / r (contiguous caches only).
+ *   workspace : only its header is used (status word; ws_bytes >= 33,024)
+ * A cache row must be written by one token only (no page shared by two rows that
+ * both append to it).
+ */
+ETA_API eta_status_t eta_append_kv(const eta_shape_t* shape, const eta_tokens_t* tokens, const eta_rope_t* rope,
+                                   void* k, void* v, const eta_pages_t* pages, const int32_t* seq_lens,
+                                   int64_t n_tokens, eta_meta_t meta, void* workspace, size_t ws_bytes,
+                                   eta_stream_t stream);
+
+/* Packed queries q [n_new][Hq][d] (q_dtype), cu_q as above; thresholds of token t
+ * and head h at tau[t * tau_stride + h] (0: per-head constants), or tau == NULL for
+ * plain softmax attention; out [n_new][Hq][d] in out_dtype (ETA_F32 or ETA_BF16),
+ * 16-byte aligned like q. The gate is params->gate with params->beta, the query's
+ * own token exempt. Nothing else of params is read. */
+typedef struct {
+  const void* q;
+  const int32_t* cu_q;
+  int64_t n_new;
+  const float* tau;
+  int64_t tau_stride;
+  void* out;
+  int32_t out_dtype;
+} eta_queries_t;
+
+/* Workspace bytes of eta_attend_window (with_prefix 0) or eta_attend_shared
+ * (with_prefix 1) for up to n_new queries on the current device; 0 for an invalid
+ * shape or count. Initialise it once with eta_workspace_init. */
+ETA_API size_t eta_attend_workspace_bytes(const eta_shape_t* shape, int64_t n_new, int32_t with_prefix);
+
+/*
+ * eta_attend_window — attention of the new tokens over a sliding window and the
+ * first tokens of their row: the query at position p sees the cached tokens
+ * s <= p with s < sinks or s > p - window (window >= 1 counts the token itself;
+ * window >= n_tokens is causal attention):
+ *   out = sum_s exp(g_s - max g) v_s / sum_s exp(g_s - max g)
+ * Tokens that no query of the row sees are not read, so the pages between the
+ * sinks and the window may be gone (blocks without a visible token take no part,
+ * whatever their table entry); values at visible tokens must be finite.
+ */
+ETA_API eta_status_t eta_attend_window(const eta_shape_t* shape, const eta_params_t* params,
+                                       const eta_queries_t* queries, const void* k, const void* v,
+                                       const eta_pages_t* pages, const int32_t* seq_lens, int64_t n_tokens,
+                                       int64_t window, int64_t sinks, void* workspace, size_t ws_bytes,
+                                       eta_stream_t stream);
+
+/* A prefix shared by every row: n_tokens tokens kept once. Contiguous: k, v
+ * [Hkv][capacity][d] (kv_dtype, 16-byte aligned). In the pools of `pages`: blocks =
+ * the page of each of its ceil(n_tokens / block_size) blocks (int32, device
+ * memory; k, v, capacity ignored). n_tokens may be 0. */
+typedef struct {
+  const void* k;
+  const void* v;
+  const int32_t* blocks;
+  int64_t capacity;
+  int64_t n_tokens;
+} eta_prefix_t;
+
+/*
+ * eta_attend_shared — attention of the new tokens over a prefix that all rows
+ * share and over their own cached tokens s <= p (p counts from the row's own first
+ * token). The prefix is read once for all rows. Every prefix token is gated when
+ * tau is given; only the query's own token is exempt.
+ */
+ETA_API eta_status_t eta_attend_shared(const eta_shape_t* shape, const eta_params_t* params,
+                                       const eta_queries_t* queries, const eta_prefix_t* prefix, const void* k,
+                                       const void* v, const eta_pages_t* pages, const int32_t* seq_lens,
+                                       int64_t n_tokens, void* workspace, size_t ws_bytes, eta_stream_t stream);
+
+/*
  * eta_test_withhold_copy — test hook of the device-timeout path; the paper has
  * no counterpart. The next decode launch in this process (any eta_decode_*
  * call) leaves the K/V copy of one admitted block unissued: position

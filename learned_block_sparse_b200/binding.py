@@ -7,6 +7,7 @@ library is missing, importing this module raises: there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -49,6 +50,27 @@ class Meta(ctypes.Structure):
 
 class Pages(ctypes.Structure):
     _fields_ = [("block_table", ctypes.c_void_p), ("num_pages", ctypes.c_int32)]
+
+
+class RopeArgs(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
+class Tokens(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("cu_new", ctypes.c_void_p), ("n_new", ctypes.c_int64)]
+
+
+class Queries(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("cu_q", ctypes.c_void_p), ("n_new", ctypes.c_int64),
+                ("tau", ctypes.c_void_p), ("tau_stride", ctypes.c_int64), ("out", ctypes.c_void_p),
+                ("out_dtype", ctypes.c_int32)]
+
+
+class PrefixArgs(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("blocks", ctypes.c_void_p),
+                ("capacity", ctypes.c_int64), ("n_tokens", ctypes.c_int64)]
 
 
 class ScreenOut(ctypes.Structure):
@@ -107,6 +129,15 @@ def _load():
     L.eta_block_stats.argtypes = [P(Shape), P(Params), vp, vp, i64, vp, i64, vp, vp, vp, vp]
     L.eta_screen_diagnostics.restype = st
     L.eta_screen_diagnostics.argtypes = [P(Shape), P(Params), i64, vp, i64, vp, vp, vp, vp, vp, vp, vp]
+    L.eta_append_kv.restype = st
+    L.eta_append_kv.argtypes = [P(Shape), P(Tokens), P(RopeArgs), vp, vp, P(Pages), vp, i64, Meta, vp, sz, vp]
+    L.eta_attend_workspace_bytes.restype = sz
+    L.eta_attend_workspace_bytes.argtypes = [P(Shape), i64, ctypes.c_int32]
+    L.eta_attend_window.restype = st
+    L.eta_attend_window.argtypes = [P(Shape), P(Params), P(Queries), vp, vp, P(Pages), vp, i64, i64, i64, vp, sz, vp]
+    L.eta_attend_shared.restype = st
+    L.eta_attend_shared.argtypes = [P(Shape), P(Params), P(Queries), P(PrefixArgs), vp, vp, P(Pages), vp, i64, vp, sz,
+                                    vp]
     L.eta_test_withhold_copy.restype = st
     L.eta_test_withhold_copy.argtypes = [i64]
     L.eta_decode_screened.restype = st
@@ -128,7 +159,8 @@ EXPORTED = ("eta_abi_version", "eta_status_string", "eta_build_block_meta", "eta
             "eta_screen_predict", "eta_decode_sparse_predict", "eta_screen_ragged", "eta_decode_sparse_ragged",
             "eta_decode_screened_ragged", "eta_decode_dense_ragged", "eta_build_block_meta_paged",
             "eta_decode_sparse_paged", "eta_decode_screened_paged", "eta_decode_dense_paged", "eta_block_stats",
-            "eta_screen_diagnostics", "eta_test_withhold_copy")
+            "eta_screen_diagnostics", "eta_test_withhold_copy", "eta_append_kv", "eta_attend_workspace_bytes",
+            "eta_attend_window", "eta_attend_shared")
 STATIC_SCRATCH_BYTES = 32 << 20
 
 
@@ -160,10 +192,26 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+_DTYPES = {ETA_F32: torch.float32, ETA_BF16: torch.bfloat16, ETA_FP8_E4M3: torch.float8_e4m3fn}
+
+
 def make_shape(batch, n_q_heads, n_kv_heads, head_dim, block_size, capacity, kv_dtype, q_dtype) -> Shape:
     return Shape(batch, n_q_heads, n_kv_heads, head_dim, block_size, capacity,
                  _dtype_code(kv_dtype) if isinstance(kv_dtype, torch.dtype) else kv_dtype,
                  _dtype_code(q_dtype) if isinstance(q_dtype, torch.dtype) else q_dtype)
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(dev: torch.device):
+    """The call's device made current; nothing to do when it is."""
+    return _HERE if dev.index is None or dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _token_stride(x: torch.Tensor) -> int:
+    """Elements between consecutive tokens (a single token's stride is not looked at)."""
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
 
 
 def make_params(beta=5.0, z=1.0, offset_a=0.0, n_local=1, n_splits=0, gate=GATE_SIGMOID, sub_blocks=1) -> Params:
@@ -387,6 +435,44 @@ def read_device_status(ws: torch.Tensor, stream=None) -> int:
     return st.value
 
 
+class Rope:
+    """Rotary positions for :meth:`EtaDecoder.append`: coordinate pair i of the first
+    ``2 * len(inv_freq)`` coordinates turns by position * inv_freq[i] (fp32, on the
+    device). Pairs are (i, i + rot_dim / 2), or neighbours with ``interleaved``."""
+
+    def __init__(self, inv_freq: torch.Tensor, interleaved: bool = False):
+        if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+            raise TypeError("inv_freq: a contiguous fp32 vector")
+        self.inv_freq = inv_freq
+        self.args = RopeArgs(inv_freq.data_ptr(), 2 * inv_freq.numel(), int(bool(interleaved)))
+
+
+_NO_ROPE = RopeArgs(None, 0, 0)
+
+
+class Prefix:
+    """A prefix of ``n_tokens`` tokens that every row shares, for
+    :meth:`EtaDecoder.shared`: ``k``, ``v`` [Hkv][capacity][d], or, in the page pools
+    of the call, ``blocks`` (int32, the page of each block of the prefix)."""
+
+    def __init__(self, n_tokens: int, k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None,
+                 blocks: Optional[torch.Tensor] = None):
+        if n_tokens < 0:
+            raise ValueError("n_tokens is negative")
+        if n_tokens > 0 and ((k is None) != (v is None) or (k is None) == (blocks is None)):
+            raise ValueError("a prefix is k and v, or blocks of the pools")
+        if k is not None:
+            if k.dim() != 3 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
+                raise ValueError("prefix k, v: two [Hkv][capacity][d] tensors of one type and device")
+            if not (k.is_contiguous() and v.is_contiguous()) or k.shape[1] < n_tokens:
+                raise ValueError("prefix k, v: contiguous, with room for n_tokens")
+        if blocks is not None and (blocks.dtype != torch.int32 or not blocks.is_contiguous()):
+            raise TypeError("prefix blocks: contiguous int32")
+        self.k, self.v, self.blocks, self.n_tokens = k, v, blocks, n_tokens
+        self.args = PrefixArgs(None if k is None else k.data_ptr(), None if v is None else v.data_ptr(),
+                               None if blocks is None else blocks.data_ptr(), 0 if k is None else k.shape[1], n_tokens)
+
+
 class EtaDecoder:
     """One attention layer's decode state: the KV cache geometry, its block
     metadata and a workspace. ``step`` runs one decode step (predictor or given
@@ -410,6 +496,8 @@ class EtaDecoder:
         self.ws = alloc_workspace(self.shape, self.params, self.device)
         self.tau = torch.empty((batch, n_q_heads), **f)
         self.out = torch.empty((batch, n_q_heads, head_dim), **f)
+        self.kv_dtype, self.q_dtype = _DTYPES[self.shape.kv_dtype], _DTYPES[self.shape.q_dtype]
+        self.attend_ws = None  # see reserve_queries
 
     @property
     def meta(self):
@@ -465,5 +553,167 @@ class EtaDecoder:
             decode_dense(self.shape, self.params, q, k, v, n_tokens, tau, tau_batch_stride or 0, o, self.ws)
         return o
 
+    # ------------------------------------------------------------- new tokens
+    def _cache_args(self, k, v, block_table, num_pages, seq_lens, cu, what):
+        """Checks of the tensors the calls for new tokens share; the page arguments."""
+        s, dev = self.shape, k.device
+        if k.dtype != self.kv_dtype or v.dtype != self.kv_dtype:
+            raise TypeError(f"{what}: K, V are not {self.kv_dtype}")
+        if block_table is None:
+            want, pages = (s.batch, s.n_kv_heads, s.capacity, s.head_dim), None
+        else:
+            num_pages = k.shape[0] if not num_pages else num_pages
+            want = (num_pages, s.n_kv_heads, s.block_size, s.head_dim)
+            if block_table.dtype != torch.int32 or not block_table.is_contiguous() or \
+                    block_table.numel() != s.batch * (s.capacity // s.block_size) or block_table.device != dev:
+                raise ValueError(f"{what}: block_table is int32 [B][capacity / block_size], contiguous, beside K")
+            pages = ctypes.byref(Pages(block_table.data_ptr(), num_pages))
+        if k.shape != want or v.shape != want or not k.is_contiguous() or not v.is_contiguous() or v.device != dev:
+            raise ValueError(f"{what}: K, V are contiguous tensors of shape {want} on one device")
+        if seq_lens is not None and (seq_lens.dtype != torch.int32 or seq_lens.numel() != s.batch or
+                                     not seq_lens.is_contiguous() or seq_lens.device != dev):
+            raise ValueError(f"{what}: seq_lens is int32 [B], contiguous, beside K")
+        if cu is not None and (cu.dtype != torch.int32 or cu.numel() != s.batch + 1 or not cu.is_contiguous() or
+                               cu.device != dev):
+            raise ValueError(f"{what}: the packed tokens' offsets are int32 [B + 1], contiguous, beside K")
+        return pages
+
+    def append(self, k_new, v_new, k, v, n_tokens: int, q: Optional[torch.Tensor] = None, rope: Optional[Rope] = None,
+               seq_lens: Optional[torch.Tensor] = None, cu_new: Optional[torch.Tensor] = None,
+               q_out: Optional[torch.Tensor] = None, block_table: Optional[torch.Tensor] = None, num_pages: int = 0,
+               build_meta: bool = True):
+        """Put new tokens into the cache ``k``, ``v`` (or, with ``block_table``, the
+        pools): keys (and ``q``) rotated by ``rope``, the metadata of the blocks that
+        became full built. ``k_new``, ``v_new`` [n][Hkv][d] and ``q`` [n][Hq][d] in
+        q_dtype: one token per row, or packed tokens with ``cu_new`` (int32 [B + 1]);
+        tokens may be strided (parts of a fused projection). Lengths (``n_tokens``,
+        ``seq_lens``) count the new tokens. Returns the rotated queries: ``q_out``, or
+        a new tensor."""
+        s, dev = self.shape, k.device
+        pages = self._cache_args(k, v, block_table, num_pages, seq_lens, cu_new, "append")
+        if block_table is not None and self.sub_blocks > 1:
+            raise EtaError(ETA_ERR_UNSUPPORTED, "eta_append_kv")
+        d, n = s.head_dim, k_new.shape[0]
+        for x, heads in ((k_new, s.n_kv_heads), (v_new, s.n_kv_heads), (q, s.n_q_heads)):
+            if x is None:
+                continue
+            if x.dtype != self.q_dtype or x.shape != (n, heads, d) or x.device != dev or x.stride(2) != 1 or \
+                    (heads > 1 and x.stride(1) != d):
+                raise ValueError(f"append: new tokens are {self.q_dtype} [n][heads][d] beside K, heads contiguous")
+        if q is not None:
+            if q_out is None:
+                q_out = torch.empty((n, s.n_q_heads, d), dtype=self.q_dtype, device=dev)
+            elif q_out.dtype != self.q_dtype or q_out.shape != q.shape or not q_out.is_contiguous() or \
+                    q_out.device != dev:
+                raise ValueError("append: q_out is contiguous, of q's shape, type and device")
+        elif q_out is not None:
+            raise ValueError("append: q_out without q")
+        tokens = Tokens(None if q is None else q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
+                        None if q is None else q_out.data_ptr(), 0 if q is None else _token_stride(q),
+                        _token_stride(k_new), _token_stride(v_new), None if cu_new is None else cu_new.data_ptr(), n)
+        meta = Meta(self.mu.data_ptr(), self.var.data_ptr(), self.maxnorm.data_ptr()) if build_meta else Meta()
+        with _on(dev):
+            _check(lib.eta_append_kv(ctypes.byref(self.meta_shape), ctypes.byref(tokens),
+                                     ctypes.byref(_NO_ROPE if rope is None else rope.args), _ptr(k), _ptr(v), pages,
+                                     _ptr(seq_lens), n_tokens, meta, _ptr(self.ws), self.ws.numel(), _stream()),
+                   "eta_append_kv")
+        return q_out
+
+    def reserve_queries(self, n: int) -> None:
+        """Workspace of :meth:`window` and :meth:`shared` for calls of up to ``n`` new
+        tokens. A larger call reserves for itself, which allocates: reserve the
+        largest before capturing a CUDA graph."""
+        with _on(self.device):
+            need = lib.eta_attend_workspace_bytes(ctypes.byref(self.shape), n, 1)
+            if need == 0:
+                raise EtaError(ETA_ERR_INVALID_ARG, "eta_attend_workspace_bytes")
+            if self.attend_ws is not None and self.attend_ws.numel() >= need:
+                return
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("reserve_queries: reserve before capturing")
+            ws = torch.empty(need + 256, dtype=torch.uint8, device=self.device)
+            off = (-ws.data_ptr()) % 256
+            ws = ws[off:off + need]
+            _check(lib.eta_workspace_init(_ptr(ws), need, _stream()), "eta_workspace_init")
+            self.attend_ws = ws
+
+    def _query_args(self, q, tau, tau_batch_stride, cu_q, out, what):
+        s, dev = self.shape, q.device
+        n = q.shape[0]
+        if q.dtype != self.q_dtype or q.shape != (n, s.n_q_heads, s.head_dim) or not q.is_contiguous():
+            raise ValueError(f"{what}: q is contiguous {self.q_dtype} [n][Hq][d]")
+        if out is None:
+            if cu_q is not None:
+                raise ValueError(f"{what}: packed queries need out")
+            out = self.out
+        if out.dtype not in (torch.float32, torch.bfloat16) or out.shape != q.shape or not out.is_contiguous() or \
+                out.device != dev:
+            raise ValueError(f"{what}: out is contiguous fp32 or bf16, of q's shape and device")
+        if tau is not None:
+            if tau.dtype != torch.float32 or not tau.is_contiguous() or tau.device != dev or \
+                    tau.shape not in ((s.n_q_heads,), (n, s.n_q_heads)):
+                raise ValueError(f"{what}: tau is contiguous fp32 [Hq] or [n][Hq] beside q")
+            if tau_batch_stride is None:
+                tau_batch_stride = 0 if tau.dim() == 1 else s.n_q_heads
+            elif tau_batch_stride not in (0, s.n_q_heads) or (tau_batch_stride and tau.dim() == 1):
+                raise ValueError(f"{what}: tau_batch_stride is 0 or Hq, within tau")
+        queries = Queries(q.data_ptr(), None if cu_q is None else cu_q.data_ptr(), n,
+                          None if tau is None else tau.data_ptr(), tau_batch_stride or 0, out.data_ptr(),
+                          ETA_F32 if out.dtype == torch.float32 else ETA_BF16)
+        return queries, out
+
+    def window(self, q, k, v, n_tokens: int, window: int, sinks: int = 0, seq_lens: Optional[torch.Tensor] = None,
+               cu_q: Optional[torch.Tensor] = None, tau: Optional[torch.Tensor] = None,
+               tau_batch_stride: Optional[int] = None, out: Optional[torch.Tensor] = None,
+               block_table: Optional[torch.Tensor] = None, num_pages: int = 0) -> torch.Tensor:
+        """Attention of new tokens over the last ``window`` tokens (their own among
+        them) and the first ``sinks`` tokens of their row. ``q`` [n][Hq][d]: one token
+        per row, or packed tokens with ``cu_q`` (int32 [B + 1]; needs ``out``). With
+        ``tau`` ([Hq] or [n][Hq]) logits are gated as in :meth:`dense`."""
+        pages = self._cache_args(k, v, block_table, num_pages, seq_lens, cu_q, "window")
+        queries, out = self._query_args(q, tau, tau_batch_stride, cu_q, out, "window")
+        if q.device != k.device:
+            raise ValueError("window: q and K are on different devices")
+        self.reserve_queries(q.shape[0])
+        with _on(q.device):
+            _check(lib.eta_attend_window(ctypes.byref(self.shape), ctypes.byref(self.params), ctypes.byref(queries),
+                                         _ptr(k), _ptr(v), pages, _ptr(seq_lens), n_tokens, window, sinks,
+                                         _ptr(self.attend_ws), self.attend_ws.numel(), _stream()),
+                   "eta_attend_window")
+        return out
+
+    def shared(self, q, k, v, n_tokens: int, prefix: Prefix, seq_lens: Optional[torch.Tensor] = None,
+               cu_q: Optional[torch.Tensor] = None, tau: Optional[torch.Tensor] = None,
+               tau_batch_stride: Optional[int] = None, out: Optional[torch.Tensor] = None,
+               block_table: Optional[torch.Tensor] = None, num_pages: int = 0) -> torch.Tensor:
+        """Attention of new tokens over a :class:`Prefix` that all rows share, read
+        once, and over their own cached tokens (``n_tokens``, ``seq_lens`` count the
+        row's own). Other arguments as :meth:`window`."""
+        pages = self._cache_args(k, v, block_table, num_pages, seq_lens, cu_q, "shared")
+        queries, out = self._query_args(q, tau, tau_batch_stride, cu_q, out, "shared")
+        s = self.shape
+        if q.device != k.device:
+            raise ValueError("shared: q and K are on different devices")
+        if prefix.n_tokens > 0:
+            if (prefix.blocks is None) != (block_table is None):
+                raise ValueError("shared: the prefix lies in the pools exactly when the rows do")
+            if prefix.k is not None and (prefix.k.dtype != self.kv_dtype or prefix.k.device != q.device or
+                                         (prefix.k.shape[0], prefix.k.shape[2]) != (s.n_kv_heads, s.head_dim)):
+                raise ValueError(f"shared: prefix k, v are {self.kv_dtype} [Hkv][capacity][d] beside q")
+            if prefix.blocks is not None and (prefix.blocks.device != q.device or
+                                              prefix.blocks.numel() < -(-prefix.n_tokens // s.block_size)):
+                raise ValueError("shared: prefix blocks cover n_tokens, beside q")
+        self.reserve_queries(q.shape[0])
+        with _on(q.device):
+            _check(lib.eta_attend_shared(ctypes.byref(s), ctypes.byref(self.params), ctypes.byref(queries),
+                                         ctypes.byref(prefix.args), _ptr(k), _ptr(v), pages, _ptr(seq_lens), n_tokens,
+                                         _ptr(self.attend_ws), self.attend_ws.numel(), _stream()),
+                   "eta_attend_shared")
+        return out
+
     def device_status(self) -> int:
-        return read_device_status(self.ws)
+        """Status of this decoder's calls since the last read, and clears it."""
+        status = read_device_status(self.ws)
+        if self.attend_ws is not None:
+            status = read_device_status(self.attend_ws) or status
+        return status

@@ -296,6 +296,54 @@ eta_status_t check_predictor(const eta_shape_t* s, const void* q, const float* W
   return ETA_OK;
 }
 
+// A packed list of new tokens: one per row without cu.
+eta_status_t check_new(const eta_shape_t* s, const int32_t* cu, int64_t n_new) {
+  if (n_new < 0 || n_new > INT32_MAX) return ETA_ERR_INVALID_ARG;
+  if (cu == nullptr) return n_new == s->batch ? ETA_OK : ETA_ERR_INVALID_ARG;
+  return aligned(cu, 4) ? ETA_OK : ETA_ERR_INVALID_ARG;
+}
+
+// Token rows of `row` elements, `stride` elements apart, read in 16-byte pieces.
+eta_status_t check_token_rows(const void* p, int64_t stride, int64_t row, int64_t elem) {
+  if (p == nullptr || !aligned(p, 16)) return ETA_ERR_INVALID_ARG;
+  return stride >= row && (stride * elem) % 16 == 0 ? ETA_OK : ETA_ERR_INVALID_ARG;
+}
+
+// The checks and fields that the attention calls of new tokens share.
+eta_status_t make_attend(const eta_shape_t* s, const eta_params_t* p, const eta_queries_t* in, const void* k,
+                         const void* v, const eta_pages_t* pages, const int32_t* seq_lens, int64_t n, void* ws,
+                         size_t ws_bytes, bool with_prefix, AttendCall* c) {
+  ETA_TRY(check_shape(s));
+  ETA_TRY(check_params(p));
+  ETA_TRY(check_tokens(s, n));
+  if (in == nullptr) return ETA_ERR_INVALID_ARG;
+  ETA_TRY(check_new(s, in->cu_q, in->n_new));
+  if (in->q == nullptr || in->out == nullptr || k == nullptr || v == nullptr) return ETA_ERR_INVALID_ARG;
+  if (!aligned(in->q, 16) || !aligned(in->out, 16) || !aligned(k, 16) || !aligned(v, 16)) return ETA_ERR_INVALID_ARG;
+  if (in->out_dtype != ETA_F32 && in->out_dtype != ETA_BF16) return ETA_ERR_INVALID_ARG;
+  if (in->tau != nullptr && (in->tau_stride < 0 || !aligned(in->tau, 4))) return ETA_ERR_INVALID_ARG;
+  if (seq_lens != nullptr) ETA_TRY(check_lens(seq_lens));
+  if (pages != nullptr) ETA_TRY(check_pages(*pages));
+  ETA_TRY(check_store_rows(s, pages != nullptr ? pages->num_pages : 0));
+  if (static_cast<int64_t>(s->batch) * s->n_kv_heads > kMaxBH) return ETA_ERR_UNSUPPORTED;
+  if (in->n_new * s->n_q_heads > INT32_MAX) return ETA_ERR_UNSUPPORTED;
+  if (ws == nullptr || !aligned(ws, 256) || ws_bytes < attend_workspace_bytes(*s, in->n_new, with_prefix))
+    return ETA_ERR_WORKSPACE;
+  std::memset(c, 0, sizeof(*c));
+  c->shape = *s;
+  c->in = *in;
+  c->beta = p->beta;
+  c->gate = p->gate;
+  c->k = k;
+  c->v = v;
+  c->block_table = pages != nullptr ? pages->block_table : nullptr;
+  c->num_pages = pages != nullptr ? pages->num_pages : 0;
+  c->seq_lens = seq_lens;
+  c->n = n;
+  c->ws = ws;
+  return ETA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -620,6 +668,90 @@ ETA_API eta_status_t eta_screen_diagnostics(const eta_shape_t* shape, const eta_
   c.active_cnt = active_cnt;
   c.out = per_head;
   return from_cuda(launch_screen_diagnostics(c, stream));
+}
+
+ETA_API eta_status_t eta_append_kv(const eta_shape_t* shape, const eta_tokens_t* tokens, const eta_rope_t* rope,
+                                   void* k, void* v, const eta_pages_t* pages, const int32_t* seq_lens,
+                                   int64_t n_tokens, eta_meta_t meta, void* workspace, size_t ws_bytes,
+                                   eta_stream_t stream) {
+  ETA_TRY(check_shape(shape));
+  ETA_TRY(check_tokens(shape, n_tokens));
+  if (tokens == nullptr || rope == nullptr) return ETA_ERR_INVALID_ARG;
+  ETA_TRY(check_new(shape, tokens->cu_new, tokens->n_new));
+  if (k == nullptr || v == nullptr || !aligned(k, 16) || !aligned(v, 16)) return ETA_ERR_INVALID_ARG;
+  const int64_t e = elem_bytes(shape->q_dtype), d = shape->head_dim;
+  if ((tokens->q == nullptr) != (tokens->q_out == nullptr)) return ETA_ERR_INVALID_ARG;
+  ETA_TRY(check_token_rows(tokens->k, tokens->k_stride, shape->n_kv_heads * d, e));
+  ETA_TRY(check_token_rows(tokens->v, tokens->v_stride, shape->n_kv_heads * d, e));
+  if (tokens->q != nullptr) {
+    ETA_TRY(check_token_rows(tokens->q, tokens->q_stride, shape->n_q_heads * d, e));
+    if (!aligned(tokens->q_out, 16)) return ETA_ERR_INVALID_ARG;
+  }
+  if (rope->rot_dim < 0 || rope->rot_dim > shape->head_dim || rope->rot_dim % 16 != 0) return ETA_ERR_INVALID_ARG;
+  if (rope->interleaved != 0 && rope->interleaved != 1) return ETA_ERR_INVALID_ARG;
+  if (rope->rot_dim > 0 && (rope->inv_freq == nullptr || !aligned(rope->inv_freq, 4))) return ETA_ERR_INVALID_ARG;
+  if (seq_lens != nullptr) ETA_TRY(check_lens(seq_lens));
+  if (pages != nullptr) ETA_TRY(check_pages(*pages));
+  ETA_TRY(check_store_rows(shape, pages != nullptr ? pages->num_pages : 0));
+  if (meta.mu != nullptr) ETA_TRY(check_meta(meta));
+  if (workspace == nullptr || !aligned(workspace, 256) || ws_bytes < kWsHeaderBytes) return ETA_ERR_WORKSPACE;
+  if (tokens->n_new == 0) return ETA_OK;
+  AppendCall c;
+  c.shape = *shape;
+  c.in = *tokens;
+  c.rope = *rope;
+  c.k = k;
+  c.v = v;
+  c.block_table = pages != nullptr ? pages->block_table : nullptr;
+  c.num_pages = pages != nullptr ? pages->num_pages : 0;
+  c.seq_lens = seq_lens;
+  c.n = n_tokens;
+  c.meta = meta;
+  c.status = static_cast<int32_t*>(workspace);
+  return from_cuda(launch_append(c, stream));
+}
+
+ETA_API size_t eta_attend_workspace_bytes(const eta_shape_t* shape, int64_t n_new, int32_t with_prefix) {
+  if (check_shape(shape) != ETA_OK || n_new < 0 || n_new > INT32_MAX) return 0;
+  return attend_workspace_bytes(*shape, n_new, with_prefix != 0);
+}
+
+ETA_API eta_status_t eta_attend_window(const eta_shape_t* shape, const eta_params_t* params,
+                                       const eta_queries_t* queries, const void* k, const void* v,
+                                       const eta_pages_t* pages, const int32_t* seq_lens, int64_t n_tokens,
+                                       int64_t window, int64_t sinks, void* workspace, size_t ws_bytes,
+                                       eta_stream_t stream) {
+  if (window < 1 || sinks < 0) return ETA_ERR_INVALID_ARG;
+  AttendCall c;
+  ETA_TRY(make_attend(shape, params, queries, k, v, pages, seq_lens, n_tokens, workspace, ws_bytes, false, &c));
+  c.window = window < n_tokens ? window : n_tokens;
+  c.sinks = sinks < n_tokens ? sinks : n_tokens;
+  if (queries->n_new == 0) return ETA_OK;
+  return from_cuda(launch_attend(c, stream));
+}
+
+ETA_API eta_status_t eta_attend_shared(const eta_shape_t* shape, const eta_params_t* params,
+                                       const eta_queries_t* queries, const eta_prefix_t* prefix, const void* k,
+                                       const void* v, const eta_pages_t* pages, const int32_t* seq_lens,
+                                       int64_t n_tokens, void* workspace, size_t ws_bytes, eta_stream_t stream) {
+  if (prefix == nullptr || prefix->n_tokens < 0 || prefix->n_tokens > INT32_MAX) return ETA_ERR_INVALID_ARG;
+  AttendCall c;
+  ETA_TRY(make_attend(shape, params, queries, k, v, pages, seq_lens, n_tokens, workspace, ws_bytes, true, &c));
+  if (prefix->n_tokens > 0) {
+    if (pages != nullptr) {
+      if (prefix->blocks == nullptr || !aligned(prefix->blocks, 4)) return ETA_ERR_INVALID_ARG;
+    } else {
+      if (prefix->k == nullptr || prefix->v == nullptr || !aligned(prefix->k, 16) || !aligned(prefix->v, 16))
+        return ETA_ERR_INVALID_ARG;
+      if (prefix->capacity < prefix->n_tokens) return ETA_ERR_INVALID_ARG;
+      if (prefix->capacity > INT32_MAX / shape->n_kv_heads) return ETA_ERR_UNSUPPORTED;
+    }
+  }
+  c.window = n_tokens;
+  c.sinks = 0;
+  c.prefix = *prefix;
+  if (queries->n_new == 0) return ETA_OK;
+  return from_cuda(launch_attend(c, stream));
 }
 
 ETA_API eta_status_t eta_test_withhold_copy(int64_t position) {

@@ -1,0 +1,422 @@
+// Appending tokens to the KV cache: rotate q and k to their positions, store k
+// and v in the cache's type, and build the metadata of the blocks that became
+// full (eta_append_kv).
+//
+// Mathematics. Coordinates (i, j) of a pair turn by a = position * inv_freq[i]:
+//   x'_i = x_i cos a - x_j sin a,  x'_j = x_j cos a + x_i sin a.
+// The angle is formed and reduced in fp64 (at position 2^20 an fp32 angle is off
+// by up to 0.06 rad), and the stored key is that rotation in fp64 rounded ONCE to
+// the cache's type: block metadata and screening decisions are built on the stored
+// bits, so they must not depend on how an fp32 intermediate happened to round.
+// Queries rotate in fp32 (their products are summed in fp32 anyway).
+//
+// What bounds it: bytes (each new q, k, v element is read once and written once)
+// for prompt chunks, launch latency for single tokens.
+//
+// Split. One thread block owns the new tokens of ONE cache block (of HB kv heads
+// and their query heads): it alone writes that block's rows, so when the block is
+// full it can build the metadata behind a __syncthreads(), with no second launch
+// and no inter-block ordering. One warp takes one token; a lane owns two 2-element
+// words of every row of the token (the two halves of its pairs), so its two angles
+// are evaluated once and serve all HB * (G + 1) rows.
+#include "common.cuh"
+#include "launch.h"
+
+namespace eta {
+
+namespace {
+
+constexpr int kAppWarps = 4;
+
+struct AppendArgs {
+  const void* q;      // [T] rows of Hq heads, q_stride elements apart (null: keys and values only)
+  const void* k;      // [T] rows of Hkv heads, k_stride
+  const void* v;      // [T] rows of Hkv heads, v_stride
+  void* q_out;        // [T][Hq][D]
+  void* kc;
+  void* vc;
+  const float* inv_freq;
+  const int32_t* block_table;
+  const int32_t* cu_new;
+  const int32_t* seq_lens;
+  float *mu, *var, *maxn;  // null: no metadata
+  int32_t* status;
+  int64_t q_stride, k_stride, v_stride, T, n, cap, nb_cap;
+  int B, Hq, Hkv, bs, bs_log2, num_pages, rot, pairs_adjacent, HB;
+};
+
+// cos and sin of a (radians, any size a position reaches): a - n * pi/2 by two
+// fused multiply-adds (pi/2 as the sum of two doubles), then the Taylor sums of
+// both functions on |r| <= pi/4, whose first omitted terms are below 3e-14.
+__device__ __forceinline__ void sincos_reduced(double a, double& s, double& c) {
+  const double n = rint(a * 0.63661977236758134308);
+  double r = fma(-n, 1.5707963267948965580, a);
+  r = fma(-n, 6.1232339957367658861e-17, r);
+  const double z = r * r;
+  double ps = 1.0 / 6227020800.0;            // 1/13!
+  ps = fma(ps, z, -1.0 / 39916800.0);
+  ps = fma(ps, z, 1.0 / 362880.0);
+  ps = fma(ps, z, -1.0 / 5040.0);
+  ps = fma(ps, z, 1.0 / 120.0);
+  ps = fma(ps, z, -1.0 / 6.0);
+  const double sr = fma(ps * z, r, r);
+  double pc = -1.0 / 87178291200.0;          // -1/14!
+  pc = fma(pc, z, 1.0 / 479001600.0);
+  pc = fma(pc, z, -1.0 / 3628800.0);
+  pc = fma(pc, z, 1.0 / 40320.0);
+  pc = fma(pc, z, -1.0 / 720.0);
+  pc = fma(pc, z, 1.0 / 24.0);
+  pc = fma(pc, z, -0.5);
+  const double cr = fma(pc, z, 1.0);
+  const int k = static_cast<int>(__double2ll_rn(n) & 3);
+  const double u = (k & 1) ? cr : sr, w = (k & 1) ? sr : cr;
+  s = (k & 2) ? -u : u;
+  c = ((k + 1) & 2) ? -w : w;
+}
+
+// fp64 -> fp32 with the last bit set when anything was cut off (round to odd):
+// a second rounding to at most 22 significant bits then gives the value rounded
+// once, because the sticky bit keeps it off that type's ties.
+__device__ __forceinline__ float to_odd(double x) {
+  const float f = __double2float_rz(x);
+  return static_cast<double>(f) == x ? f : __int_as_float(__float_as_int(f) | 1);
+}
+
+__device__ __forceinline__ uint32_t bf16_bits(float x) {
+  uint16_t r;
+  asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(r) : "f"(x));
+  return r;
+}
+
+// A word: two neighbouring coordinates of a row.
+template <typename T>
+__device__ __forceinline__ float2 load_word(const void* p, int64_t elem);
+template <>
+__device__ __forceinline__ float2 load_word<Bf16Raw>(const void* p, int64_t elem) {
+  const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p) + elem));
+  return make_float2(bf16_lo(w), bf16_hi(w));
+}
+template <>
+__device__ __forceinline__ float2 load_word<float>(const void* p, int64_t elem) {
+  return __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(p) + elem));
+}
+
+// Store two fp32 values (already on the odd-rounding path where that matters).
+template <typename T>
+__device__ __forceinline__ void store_word(void* p, int64_t elem, float x, float y);
+template <>
+__device__ __forceinline__ void store_word<float>(void* p, int64_t elem, float x, float y) {
+  *reinterpret_cast<float2*>(static_cast<float*>(p) + elem) = make_float2(x, y);
+}
+template <>
+__device__ __forceinline__ void store_word<Bf16Raw>(void* p, int64_t elem, float x, float y) {
+  *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p) + elem) = bf16_bits(x) | (bf16_bits(y) << 16);
+}
+template <>
+__device__ __forceinline__ void store_word<Fp8Raw>(void* p, int64_t elem, float x, float y) {
+  uint16_t r;  // nearest even, values past 448 saturate
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(y), "f"(x));
+  *reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(p) + elem) = r;
+}
+
+// One rotated coordinate in the cache's type: correctly rounded from fp64.
+template <typename KV>
+__device__ __forceinline__ float key_value(double x) { return to_odd(x); }
+template <>
+__device__ __forceinline__ float key_value<float>(double x) { return __double2float_rn(x); }
+
+template <typename KV>
+__device__ __forceinline__ float cache_elem(uint32_t w, int p);
+template <>
+__device__ __forceinline__ float cache_elem<float>(uint32_t w, int) { return __uint_as_float(w); }
+template <>
+__device__ __forceinline__ float cache_elem<Bf16Raw>(uint32_t w, int p) { return p == 0 ? bf16_lo(w) : bf16_hi(w); }
+template <>
+__device__ __forceinline__ float cache_elem<Fp8Raw>(uint32_t w, int p) { return e4m3_to_float((w >> (8 * p)) & 0xffu); }
+
+// The metadata of a full block, split over the warps of a thread block: part 0
+// the row norms (lane = row), parts 1..WL the column sums of 32 words each
+// (lane = word). Every sum runs in the order eta_build_block_meta documents
+// (rows and coordinates increasing, fused multiply-adds), so both give the same
+// bits. Plain loads: the rows were written by this thread block.
+template <typename KV, int D>
+__device__ __forceinline__ void meta_part(const unsigned char* base, int bs, int part, int lane, float* mu, float* var,
+                                          float* maxn, int64_t col, int64_t nb_cap) {
+  constexpr int EB = KvTraits<KV>::kBytes;
+  constexpr int P = 4 / EB;         // coordinates per 32-bit word
+  constexpr int WPR = D / P;        // words per row
+  const float rows = static_cast<float>(bs);
+  if (part == 0) {
+    float best = 0.0f;
+    for (int r = lane; r < bs; r += 32) {
+      const uint4* row = reinterpret_cast<const uint4*>(base + static_cast<int64_t>(r) * D * EB);
+      float nr = 0.0f;
+#pragma unroll
+      for (int c = 0; c < D * EB / 16; ++c) {
+        const uint4 u = row[c];
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int p = 0; p < P; ++p) {
+            const float x = cache_elem<KV>(w[i], p);
+            nr = __fmaf_rn(x, x, nr);
+          }
+      }
+      best = fmaxf(best, nr);
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) best = fmaxf(best, __shfl_xor_sync(kFull, best, o));
+    if (lane == 0) *maxn = __fsqrt_rn(best);
+    return;
+  }
+  const uint32_t* words = reinterpret_cast<const uint32_t*>(base) + (part - 1) * 32 + lane;
+  float t[P], v[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) t[p] = v[p] = 0.0f;
+#pragma unroll 16
+  for (int r = 0; r < bs; ++r) {
+    const uint32_t w = words[static_cast<int64_t>(r) * WPR];
+#pragma unroll
+    for (int p = 0; p < P; ++p) t[p] = __fadd_rn(t[p], cache_elem<KV>(w, p));
+  }
+#pragma unroll
+  for (int p = 0; p < P; ++p) t[p] = __fdiv_rn(t[p], rows);
+#pragma unroll 16
+  for (int r = 0; r < bs; ++r) {
+    const uint32_t w = words[static_cast<int64_t>(r) * WPR];
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const float e = __fsub_rn(cache_elem<KV>(w, p), t[p]);
+      v[p] = __fmaf_rn(e, e, v[p]);
+    }
+  }
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const int64_t o = static_cast<int64_t>(((part - 1) * 32 + lane) * P + p) * nb_cap + col;
+    mu[o] = t[p];
+    var[o] = __fdiv_rn(v[p], rows);
+  }
+}
+
+template <typename QT, typename KV, int D>
+__global__ void __launch_bounds__(kAppWarps * 32) append_kernel(const AppendArgs a) {
+  constexpr int EB = KvTraits<KV>::kBytes;
+  constexpr int LPR = D / 4;        // lanes per row: each owns two words
+  constexpr int RPW = 32 / LPR;     // rows a warp works on at once
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int item = blockIdx.x, bs = a.bs, sh = a.bs_log2;
+  grid_dependency_wait();
+  allow_dependent_launch();
+
+  // Row and cache block of this item. Row b's blocks take the items from
+  // s_b = floor(cu[b] / bs) + 2 b on: n_b new tokens touch at most
+  // floor(n_b / bs) + 2 blocks <= s_{b+1} - s_b, so no prefix sum is needed.
+  int b = item;
+  int64_t t0 = item, fresh = 1, j = 0;
+  if (a.cu_new != nullptr) {
+    if (threadIdx.x == 0 && blockIdx.y == 0 && item < a.B) {  // every row's bounds are looked at once
+      const int64_t c0 = a.cu_new[item], c1 = a.cu_new[item + 1];
+      if (c0 < 0 || c1 < c0 || c1 > a.T) atomicExch(a.status, static_cast<int32_t>(ETA_ERR_INVALID_ARG));
+    }
+    int lo = 0, hi = a.B - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if ((static_cast<int64_t>(__ldg(a.cu_new + mid)) >> sh) + 2 * static_cast<int64_t>(mid) <= item) lo = mid;
+      else hi = mid - 1;
+    }
+    b = lo;
+    t0 = __ldg(a.cu_new + b);
+    fresh = __ldg(a.cu_new + b + 1) - t0;
+    if (t0 < 0 || fresh <= 0 || t0 + fresh > a.T) return;
+    j = item - ((t0 >> sh) + 2 * static_cast<int64_t>(b));
+    if (j < 0) return;
+  }
+  const int64_t len = a.seq_lens != nullptr ? static_cast<int64_t>(__ldg(a.seq_lens + b)) : a.n;
+  if (len == 0 && a.cu_new == nullptr) return;  // an idle row of a padded batch
+  if (len < fresh || len > a.n) {
+    if (threadIdx.x == 0) atomicExch(a.status, static_cast<int32_t>(ETA_ERR_INVALID_ARG));
+    return;
+  }
+  const int64_t first = len - fresh;
+  const int64_t blk = (first >> sh) + j;
+  const int64_t slot0 = max(first, blk << sh), slot1 = min(len, (blk + 1) << sh);
+  if (slot0 >= slot1) return;
+
+  const int kv0 = blockIdx.y * a.HB;
+  const int nkv = min(a.HB, a.Hkv - kv0), G = a.Hq / a.Hkv;
+  // store row of the block's token 0 for kv head kv0, and the rows between heads
+  int64_t row0, head_rows;
+  bool page_ok = true;
+  if (a.block_table != nullptr) {
+    const int page = __ldg(a.block_table + static_cast<int64_t>(b) * a.nb_cap + blk);
+    page_ok = page >= 0 && page < a.num_pages;
+    if (!page_ok && threadIdx.x == 0) atomicExch(a.status, static_cast<int32_t>(ETA_ERR_INVALID_ARG));
+    row0 = (static_cast<int64_t>(page_ok ? page : 0) * a.Hkv + kv0) * bs;
+    head_rows = bs;
+  } else {
+    row0 = (static_cast<int64_t>(b) * a.Hkv + kv0) * a.cap + (blk << sh);
+    head_rows = a.cap;
+  }
+
+  // This lane's two words: the halves of its pairs (or two adjacent pairs) inside
+  // the rotated part, neighbouring words past it.
+  const int quarter = a.rot >> 2;
+  const int w = lane % LPR, sub = lane / LPR;
+  const bool turns = w < quarter;
+  const int e0 = turns ? 2 * w : 2 * quarter * 2 + 4 * (w - quarter);
+  const int e1 = turns ? 2 * (w + quarter) : e0 + 2;
+  double f0 = 0.0, f1 = 0.0;
+  if (turns) {
+    f0 = __ldg(a.inv_freq + (a.pairs_adjacent ? w : 2 * w));
+    f1 = __ldg(a.inv_freq + (a.pairs_adjacent ? w + quarter : 2 * w + 1));
+  }
+  const int rows = nkv * (G + 2);  // per kv head: the key, the value, G queries
+
+  for (int64_t slot = slot0 + warp; slot < slot1; slot += kAppWarps) {
+    const int64_t tok = t0 + (slot - first);
+    double s0 = 0.0, c0 = 1.0, s1 = 0.0, c1 = 1.0;
+    if (turns) {
+      sincos_reduced(static_cast<double>(slot) * f0, s0, c0);
+      sincos_reduced(static_cast<double>(slot) * f1, s1, c1);
+    }
+    const float s0f = static_cast<float>(s0), c0f = static_cast<float>(c0);
+    const float s1f = static_cast<float>(s1), c1f = static_cast<float>(c1);
+    constexpr int U = 4;  // rows in flight per lane
+    for (int r0 = 0; r0 < rows; r0 += U * RPW) {
+      float2 x[U], y[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int r = r0 + u * RPW + sub;
+        x[u] = y[u] = make_float2(0.0f, 0.0f);
+        if (r >= rows) continue;
+        const int h = r / (G + 2), g = r - h * (G + 2);
+        const void* src = g == 0 ? a.k : (g == 1 ? a.v : a.q);
+        if (src == nullptr) continue;
+        const int64_t at = g == 0 ? tok * a.k_stride + static_cast<int64_t>(kv0 + h) * D
+                                  : (g == 1 ? tok * a.v_stride + static_cast<int64_t>(kv0 + h) * D
+                                            : tok * a.q_stride + static_cast<int64_t>((kv0 + h) * G + g - 2) * D);
+        x[u] = load_word<QT>(src, at + e0);
+        y[u] = load_word<QT>(src, at + e1);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int r = r0 + u * RPW + sub;
+        if (r >= rows) continue;
+        const int h = r / (G + 2), g = r - h * (G + 2);
+        if (g <= 1) {
+          if (!page_ok) continue;
+          const int64_t at = (row0 + static_cast<int64_t>(h) * head_rows + (slot - (blk << sh))) * D;
+          if (g == 1 || !turns) {
+            void* dst = g == 1 ? a.vc : a.kc;
+            store_word<KV>(dst, at + e0, x[u].x, x[u].y);
+            store_word<KV>(dst, at + e1, y[u].x, y[u].y);
+          } else if (a.pairs_adjacent) {
+            const double p = x[u].x, q = x[u].y, m = y[u].x, n = y[u].y;
+            store_word<KV>(a.kc, at + e0, key_value<KV>(fma(p, c0, -(q * s0))), key_value<KV>(fma(q, c0, p * s0)));
+            store_word<KV>(a.kc, at + e1, key_value<KV>(fma(m, c1, -(n * s1))), key_value<KV>(fma(n, c1, m * s1)));
+          } else {
+            const double p = x[u].x, q = x[u].y, m = y[u].x, n = y[u].y;
+            store_word<KV>(a.kc, at + e0, key_value<KV>(fma(p, c0, -(m * s0))), key_value<KV>(fma(q, c1, -(n * s1))));
+            store_word<KV>(a.kc, at + e1, key_value<KV>(fma(m, c0, p * s0)), key_value<KV>(fma(n, c1, q * s1)));
+          }
+        } else if (a.q != nullptr) {
+          const int64_t at = (tok * a.Hq + (kv0 + h) * G + g - 2) * D;
+          float2 p = x[u], q = y[u];
+          if (turns && a.pairs_adjacent) {
+            p = make_float2(x[u].x * c0f - x[u].y * s0f, x[u].y * c0f + x[u].x * s0f);
+            q = make_float2(y[u].x * c1f - y[u].y * s1f, y[u].y * c1f + y[u].x * s1f);
+          } else if (turns) {
+            p = make_float2(x[u].x * c0f - y[u].x * s0f, x[u].y * c1f - y[u].y * s1f);
+            q = make_float2(y[u].x * c0f + x[u].x * s0f, y[u].y * c1f + x[u].y * s1f);
+          }
+          store_word<QT>(a.q_out, at + e0, p.x, p.y);
+          store_word<QT>(a.q_out, at + e1, q.x, q.y);
+        }
+      }
+    }
+  }
+
+  if (a.mu == nullptr || !page_ok || slot1 != ((blk + 1) << sh)) return;  // (uniform over the thread block)
+  __syncthreads();  // the block's last rows are written
+  constexpr int kParts = 1 + D * EB / 128;
+  for (int i = warp; i < nkv * kParts; i += kAppWarps) {
+    const int h = i / kParts, part = i - h * kParts;
+    const unsigned char* base =
+        static_cast<const unsigned char*>(a.kc) + (row0 + static_cast<int64_t>(h) * head_rows) * D * EB;
+    const int64_t seg = static_cast<int64_t>(b) * a.Hkv + kv0 + h;
+    meta_part<KV, D>(base, bs, part, lane, a.mu + seg * D * a.nb_cap, a.var + seg * D * a.nb_cap,
+                     a.maxn + seg * a.nb_cap + blk, blk, a.nb_cap);
+  }
+}
+
+template <typename QT, typename KV>
+cudaError_t launch_append_t(const AppendArgs& a, int D, int64_t items, cudaStream_t st) {
+  dim3 grid(static_cast<unsigned>(items), static_cast<unsigned>((a.Hkv + a.HB - 1) / a.HB));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kAppWarps * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1] = {pdl_attribute()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e;
+  if constexpr (KvTraits<KV>::kBytes == 1) {
+    e = cudaLaunchKernelEx(&cfg, append_kernel<QT, KV, 128>, a);
+  } else {
+    e = D == 128 ? cudaLaunchKernelEx(&cfg, append_kernel<QT, KV, 128>, a)
+                 : cudaLaunchKernelEx(&cfg, append_kernel<QT, KV, 64>, a);
+  }
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_append(const AppendCall& c, cudaStream_t st) {
+  const eta_shape_t& s = c.shape;
+  AppendArgs a;
+  a.q = c.in.q;
+  a.k = c.in.k;
+  a.v = c.in.v;
+  a.q_out = c.in.q_out;
+  a.kc = c.k;
+  a.vc = c.v;
+  a.inv_freq = c.rope.inv_freq;
+  a.rot = c.rope.rot_dim;
+  a.pairs_adjacent = c.rope.interleaved;
+  a.block_table = c.block_table;
+  a.num_pages = c.num_pages;
+  a.cu_new = c.in.cu_new;
+  a.seq_lens = c.seq_lens;
+  a.mu = c.meta.mu;
+  a.var = c.meta.var;
+  a.maxn = c.meta.maxnorm;
+  a.status = c.status;
+  a.q_stride = c.in.q_stride;
+  a.k_stride = c.in.k_stride;
+  a.v_stride = c.in.v_stride;
+  a.T = c.in.n_new;
+  a.n = c.n;
+  a.cap = s.capacity;
+  a.nb_cap = s.capacity / s.block_size;
+  a.B = s.batch;
+  a.Hq = s.n_q_heads;
+  a.Hkv = s.n_kv_heads;
+  a.bs = s.block_size;
+  a.bs_log2 = 0;
+  while ((1 << a.bs_log2) < s.block_size) ++a.bs_log2;
+  const int64_t items = a.cu_new == nullptr ? s.batch : a.T / a.bs + 2 * static_cast<int64_t>(s.batch);
+  a.HB = 1;
+  const bool qf32 = s.q_dtype == ETA_F32;
+  switch (s.kv_dtype) {
+    case ETA_FP8_E4M3: return launch_append_t<Bf16Raw, Fp8Raw>(a, s.head_dim, items, st);
+    case ETA_BF16:
+      return qf32 ? launch_append_t<float, Bf16Raw>(a, s.head_dim, items, st)
+                  : launch_append_t<Bf16Raw, Bf16Raw>(a, s.head_dim, items, st);
+    default:
+      return qf32 ? launch_append_t<float, float>(a, s.head_dim, items, st)
+                  : launch_append_t<Bf16Raw, float>(a, s.head_dim, items, st);
+  }
+}
+
+}  // namespace eta

@@ -1,0 +1,195 @@
+// Pieces shared by the attention kernels of new tokens (eta_attend_window,
+// eta_attend_shared): arguments, the mapping of tiles to rows of packed queries,
+// the visible ranges of a tile, the gate, and the layout of partial results.
+//
+// A call is at most two passes of tiles over keys and a merge. The OWN pass takes
+// the queries of one row (all heads of a group: tile rows = queries x G) over the
+// row's cached tokens they can see; the PREFIX pass takes the packed queries of
+// all rows over the shared prefix. A tile's keys may be split into `splits` equal
+// ranges of key tiles; each range leaves an unnormalised partial (o, running max
+// in log2 units, sum) in its own slot, and the merge adds the slots of every
+// (token, head) in slot order, so results do not depend on the order in which
+// thread blocks run. A call with one slot writes the output directly.
+#pragma once
+
+#include <cmath>
+
+#include "common.cuh"
+#include "launch.h"
+
+namespace eta {
+
+struct AttendArgs {
+  const void* q;   // [T][Hq][D]
+  const void* k;   // the rows' cache or pool
+  const void* v;
+  const void* pk;  // the shared prefix (contiguous: [Hkv][pcap][D]; else the pool)
+  const void* pv;
+  const int32_t* block_table;
+  const int32_t* pblocks;  // pages of the prefix, or null: contiguous
+  const int32_t* cu_q;
+  const int32_t* seq_lens;
+  const float* tau;
+  void* out;
+  float* o_part;    // [slots][T * Hq][D]
+  float2* ml_part;  // [slots][T * Hq]
+  int32_t* status;
+  int64_t T, n, cap, nb_cap, pcap, P, window, sinks, tau_stride;
+  int B, Hq, Hkv, G, bs, bs_log2, num_pages, q_dtype, out_dtype, gate;
+  int own_splits, prefix_splits;  // slots: the own pass's, then the prefix pass's
+  float beta, qscale;
+};
+
+// One tile of the own pass: nq packed queries of row b from token tok0 on, the
+// first at cache position p0.
+struct OwnTile {
+  int b, nq;
+  int64_t tok0, p0;
+};
+
+// Tile `item` of the own pass, 2^qt_log2 queries per tile. Row b's tiles take the
+// items from floor(cu[b] / QT) + b on: ceil(n_b / QT) of them, which is at most
+// the distance to the next row's first, so no prefix sum is needed (items in
+// between are empty). False: nothing to do.
+__device__ __forceinline__ bool own_tile(const AttendArgs& a, int item, int qt_log2, bool report, OwnTile& t) {
+  int64_t fresh = 1, first = item, j = 0;
+  t.b = item;
+  if (a.cu_q != nullptr) {
+    if (report && item < a.B) {  // every row's bounds are looked at once
+      const int64_t c0 = a.cu_q[item], c1 = a.cu_q[item + 1];
+      if (c0 < 0 || c1 < c0 || c1 > a.T) atomicExch(a.status, static_cast<int32_t>(ETA_ERR_INVALID_ARG));
+    }
+    int lo = 0, hi = a.B - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if ((static_cast<int64_t>(__ldg(a.cu_q + mid)) >> qt_log2) + mid <= item) lo = mid;
+      else hi = mid - 1;
+    }
+    t.b = lo;
+    first = __ldg(a.cu_q + lo);
+    fresh = __ldg(a.cu_q + lo + 1) - first;
+    if (first < 0 || fresh <= 0 || first + fresh > a.T) return false;
+    j = item - ((first >> qt_log2) + lo);
+    if (j < 0 || (j << qt_log2) >= fresh) return false;
+  }
+  const int64_t len = a.seq_lens != nullptr ? static_cast<int64_t>(__ldg(a.seq_lens + t.b)) : a.n;
+  if (len == 0 && a.cu_q == nullptr) return false;  // an idle row
+  if (len < fresh || len > a.n) {
+    if (report) atomicExch(a.status, static_cast<int32_t>(ETA_ERR_INVALID_ARG));
+    return false;
+  }
+  const int64_t q0 = j << qt_log2;
+  t.tok0 = first + q0;
+  t.nq = static_cast<int>(min(fresh - q0, int64_t{1} << qt_log2));
+  t.p0 = len - fresh + q0;
+  return true;
+}
+
+// Whether packed token t belongs to a row whose queries the own pass computes.
+__device__ __forceinline__ bool token_live(const AttendArgs& a, int64_t t) {
+  int b = static_cast<int>(t);
+  int64_t fresh = 1;
+  if (a.cu_q != nullptr) {
+    int lo = 0, hi = a.B - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (__ldg(a.cu_q + mid) <= t) lo = mid;
+      else hi = mid - 1;
+    }
+    b = lo;
+    const int64_t c0 = __ldg(a.cu_q + b), c1 = __ldg(a.cu_q + b + 1);
+    if (c0 < 0 || c1 > a.T || t < c0 || t >= c1) return false;
+    fresh = c1 - c0;
+  }
+  const int64_t len = a.seq_lens != nullptr ? static_cast<int64_t>(__ldg(a.seq_lens + b)) : a.n;
+  return len >= fresh && len <= a.n;
+}
+
+// The positions that queries p0 .. p1 of a row see, as two ranges [0, a1) (sinks
+// before the window) and [b0, b1); one range when they touch.
+struct Visible {
+  int64_t a1, b0, b1;
+};
+__device__ __forceinline__ Visible visible_of(const AttendArgs& a, int64_t p0, int64_t p1) {
+  Visible r;
+  r.b0 = max(int64_t{0}, p0 - a.window + 1);
+  r.b1 = p1 + 1;
+  r.a1 = min(a.sinks, r.b0);
+  if (r.a1 == r.b0) r.a1 = r.b0 = 0;
+  return r;
+}
+
+// Row, in a [rows][D] view of the store, of cache position s of row b, kv head h;
+// -1: its page is outside the pool.
+__device__ __forceinline__ int64_t own_row(const AttendArgs& a, int b, int h, int64_t s) {
+  if (a.block_table == nullptr) return (static_cast<int64_t>(b) * a.Hkv + h) * a.cap + s;
+  const int page = __ldg(a.block_table + static_cast<int64_t>(b) * a.nb_cap + (s >> a.bs_log2));
+  if (page < 0 || page >= a.num_pages) return -1;
+  return (static_cast<int64_t>(page) * a.Hkv + h) * a.bs + (s & (a.bs - 1));
+}
+__device__ __forceinline__ int64_t prefix_row(const AttendArgs& a, int h, int64_t s) {
+  if (a.pblocks == nullptr) return static_cast<int64_t>(h) * a.pcap + s;
+  const int page = __ldg(a.pblocks + (s >> a.bs_log2));
+  if (page < 0 || page >= a.num_pages) return -1;
+  return (static_cast<int64_t>(page) * a.Hkv + h) * a.bs + (s & (a.bs - 1));
+}
+
+__device__ __forceinline__ void store_out(void* out, int dtype, int64_t i, float x) {
+  if (dtype == ETA_F32) {
+    static_cast<float*>(out)[i] = x;
+  } else {
+    uint16_t r;
+    asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(r) : "f"(x));
+    static_cast<uint16_t*>(out)[i] = r;
+  }
+}
+
+inline AttendArgs make_attend_args(const AttendCall& c) {
+  const eta_shape_t& s = c.shape;
+  AttendArgs a;
+  a.q = c.in.q;
+  a.k = c.k;
+  a.v = c.v;
+  const bool paged = c.block_table != nullptr;
+  a.pk = paged ? c.k : c.prefix.k;
+  a.pv = paged ? c.v : c.prefix.v;
+  a.block_table = c.block_table;
+  a.pblocks = paged ? c.prefix.blocks : nullptr;
+  a.cu_q = c.in.cu_q;
+  a.seq_lens = c.seq_lens;
+  a.tau = c.in.tau;
+  a.out = c.in.out;
+  a.o_part = nullptr;
+  a.ml_part = nullptr;
+  a.status = static_cast<int32_t*>(c.ws);
+  a.T = c.in.n_new;
+  a.n = c.n;
+  a.cap = s.capacity;
+  a.nb_cap = s.capacity / s.block_size;
+  a.pcap = c.prefix.capacity;
+  a.P = c.prefix.n_tokens;
+  a.window = c.window;
+  a.sinks = c.sinks;
+  a.tau_stride = c.in.tau_stride;
+  a.B = s.batch;
+  a.Hq = s.n_q_heads;
+  a.Hkv = s.n_kv_heads;
+  a.G = s.n_q_heads / s.n_kv_heads;
+  a.bs = s.block_size;
+  a.bs_log2 = 0;
+  while ((1 << a.bs_log2) < s.block_size) ++a.bs_log2;
+  a.num_pages = c.num_pages;
+  a.q_dtype = s.q_dtype;
+  a.out_dtype = c.in.out_dtype;
+  a.gate = c.gate;
+  a.own_splits = a.prefix_splits = 1;
+  a.beta = c.beta;
+  a.qscale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(s.head_dim)));
+  return a;
+}
+
+// The passes, one launch each (grids from the arguments).
+cudaError_t launch_attend_simt(const AttendArgs& a, int kv_dtype, int D, bool prefix, cudaStream_t st);
+cudaError_t launch_attend_merge(const AttendArgs& a, int D, cudaStream_t st);
+
+}  // namespace eta

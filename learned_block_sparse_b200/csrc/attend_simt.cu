@@ -1,0 +1,274 @@
+// Attention of new tokens on the CUDA cores, in fp32 throughout: any cache and
+// query type, any tile. It serves the fp32 caches (and fp32 queries), whose
+// results keep fp32 precision; bf16 and fp8 caches have the tensor-core kernels.
+//
+// One thread block takes 16 tile rows (queries x the G heads of a group) over a
+// range of 32-key tiles. Keys and values are widened to fp32 in shared memory
+// (rows padded by 16 bytes: the eight lanes of a 128-bit load hit eight bank
+// groups), the next tile's 16-byte pieces are already in registers while this one
+// is attended. Scores: lane = key, warp w takes rows w and w + 8. The softmax of a
+// row stays inside its warp. Values: a thread owns one output column and a share
+// of the keys for all rows.
+//
+// Bound: HBM for few rows (one 32 KB tile costs ~1,400 cycles of an SM's HBM share
+// and ~800 cycles of work for a single row), the shared-memory and FMA pipes for
+// full tiles.
+#include "attend_common.cuh"
+
+namespace eta {
+
+namespace {
+
+constexpr int kThr = 256, kKT = 32, kR = 16;  // threads, keys per tile, rows per tile
+
+template <typename KV>
+__device__ __forceinline__ void widen_piece(const uint4& w, float* x) { widen16<KV>(w, x); }
+template <>
+__device__ __forceinline__ void widen_piece<Fp8Raw>(const uint4& w, float* x) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = e4m3_to_float((u[i >> 2] >> (8 * (i & 3))) & 0xffu);
+}
+
+template <typename KV, int D, bool PREFIX>
+__global__ void __launch_bounds__(kThr) attend_simt_kernel(const AttendArgs a) {
+  constexpr int EB = KvTraits<KV>::kBytes;
+  constexpr int CPR = D * EB / 16;          // 16-byte pieces per row
+  constexpr int EPP = 16 / EB;              // elements per piece
+  constexpr int NCH = 2 * kKT * CPR / kThr; // pieces per thread and tile (K and V)
+  constexpr int LD = D + 4;
+  constexpr int PARTS = kThr / D;           // key shares of the value pass
+  __shared__ __align__(16) float s_k[kKT * LD];
+  __shared__ __align__(16) float s_v[kKT * LD];
+  __shared__ __align__(16) float s_q[kR * D];
+  __shared__ __align__(16) float s_p[kR * kKT];
+  __shared__ float s_corr[kR];
+  __shared__ int s_ok[kKT];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int h = blockIdx.y, G = a.G;
+  grid_dependency_wait();
+  allow_dependent_launch();
+
+  const int qt = kR / G;  // queries per tile (a power of two)
+  int qt_log2 = 0;
+  while ((1 << qt_log2) < qt) ++qt_log2;
+  OwnTile t;
+  Visible vis;
+  int64_t tiles, tiles_a = 0;
+  const int split = blockIdx.z, splits = PREFIX ? a.prefix_splits : a.own_splits;
+  if (PREFIX) {
+    t.b = 0;
+    t.tok0 = static_cast<int64_t>(blockIdx.x) * qt;
+    t.nq = static_cast<int>(min(a.T - t.tok0, static_cast<int64_t>(qt)));
+    t.p0 = 0;
+    vis.a1 = vis.b0 = 0;
+    vis.b1 = a.P;
+    tiles = (a.P + kKT - 1) / kKT;
+  } else {
+    if (!own_tile(a, blockIdx.x, qt_log2, tid == 0 && h == 0 && split == 0, t)) return;
+    vis = visible_of(a, t.p0, t.p0 + t.nq - 1);
+    tiles_a = (vis.a1 + kKT - 1) / kKT;
+    tiles = tiles_a + (vis.b1 - vis.b0 + kKT - 1) / kKT;
+  }
+  const int64_t u0 = tiles * split / splits, u1 = tiles * (split + 1) / splits;
+  const int rows = t.nq * G;  // tile row r: query r / G, head h * G + r % G
+
+  for (int i = tid; i < rows * D; i += kThr) {
+    const int r = i / D;
+    const int64_t row = (t.tok0 + r / G) * a.Hq + h * G + r % G;
+    s_q[i] = load_elem(a.q, a.q_dtype, row * D + i % D) * a.qscale;
+  }
+
+  // first key and end of key tile u
+  auto bounds = [&](int64_t u, int64_t& s0, int64_t& s1) {
+    if (u < tiles_a) {
+      s0 = u * kKT;
+      s1 = min(vis.a1, s0 + kKT);
+    } else {
+      s0 = vis.b0 + (u - tiles_a) * kKT;
+      s1 = min(vis.b1, s0 + kKT);
+    }
+  };
+  uint4 piece[NCH];
+  int ok_bits = 0;  // piece i's key is inside the tile and its page inside the pool
+  auto fetch = [&](int64_t u) {
+    int64_t s0, s1;
+    bounds(u, s0, s1);
+    ok_bits = 0;
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      const int idx = tid + i * kThr;
+      const int which = idx / (kKT * CPR), key = (idx / CPR) % kKT, c = idx % CPR;
+      piece[i] = make_uint4(0u, 0u, 0u, 0u);
+      const int64_t s = s0 + key;
+      if (s >= s1) continue;
+      const int64_t row = PREFIX ? prefix_row(a, h, s) : own_row(a, t.b, h, s);
+      if (row < 0) {
+        atomicExch(a.status, static_cast<int32_t>(ETA_ERR_INVALID_ARG));
+        continue;
+      }
+      const void* base = which == 0 ? (PREFIX ? a.pk : a.k) : (PREFIX ? a.pv : a.v);
+      piece[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(base) + row * D * EB) + c);
+      ok_bits |= 1 << i;
+    }
+  };
+
+  // this warp's two rows: w and w + 8
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, tau[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = warp + 8 * i;
+    if (r < rows && a.tau != nullptr) tau[i] = a.tau[(t.tok0 + r / G) * a.tau_stride + h * G + r % G];
+  }
+  float acc[kR];
+#pragma unroll
+  for (int r = 0; r < kR; ++r) acc[r] = 0.0f;
+  const int col = tid % D, part = tid / D;
+
+  if (u0 < u1) fetch(u0);
+  for (int64_t u = u0; u < u1; ++u) {
+    __syncthreads();  // the previous tile is done with
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      const int idx = tid + i * kThr;
+      const int which = idx / (kKT * CPR), key = (idx / CPR) % kKT, c = idx % CPR;
+      float x[EPP];
+      widen_piece<KV>(piece[i], x);
+      float* dst = (which == 0 ? s_k : s_v) + key * LD + c * EPP;
+#pragma unroll
+      for (int e = 0; e < EPP; e += 4)
+        *reinterpret_cast<float4*>(dst + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+      if (which == 0 && c == 0) s_ok[key] = (ok_bits >> i) & 1;
+    }
+    __syncthreads();
+    if (u + 1 < u1) fetch(u + 1);
+    int64_t s0, s1;
+    bounds(u, s0, s1);
+    const int64_t s = s0 + lane;
+    const bool there = s < s1 && s_ok[lane] != 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = warp + 8 * i;
+      if (r >= rows) break;
+      const float4* q4 = reinterpret_cast<const float4*>(s_q + r * D);
+      const float4* k4 = reinterpret_cast<const float4*>(s_k + lane * LD);
+      float d0 = 0.0f, d1 = 0.0f, d2 = 0.0f, d3 = 0.0f;
+#pragma unroll 8
+      for (int c = 0; c < D / 4; ++c) {
+        const float4 x = q4[c], y = k4[c];
+        d0 = fmaf(x.x, y.x, d0);
+        d1 = fmaf(x.y, y.y, d1);
+        d2 = fmaf(x.z, y.z, d2);
+        d3 = fmaf(x.w, y.w, d3);
+      }
+      const float S = (d0 + d1) + (d2 + d3);
+      const int64_t p = t.p0 + r / G;
+      bool see = there;
+      if (!PREFIX) see = see && s <= p && (s < a.sinks || s > p - a.window);
+      float g = S;
+      if (a.tau != nullptr && (PREFIX || s != p)) {
+        if (a.gate == ETA_GATE_HARD) g = S >= tau[i] ? S : -INFINITY;
+        else g = S / (1.0f + expf(-a.beta * (S - tau[i])));
+      }
+      g = see ? g * kLog2e : -INFINITY;
+      float mx = g;
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+      const float mn = fmaxf(m[i], mx);
+      const float pr = mn == -INFINITY ? 0.0f : exp2f(g - mn);
+      const float corr = mn == -INFINITY ? 1.0f : exp2f(m[i] - mn);
+      float sum = pr;
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+      l[i] = fmaf(l[i], corr, sum);
+      m[i] = mn;
+      s_p[r * kKT + lane] = pr;
+      if (lane == 0) s_corr[r] = corr;
+    }
+    __syncthreads();
+    constexpr int KS = kKT / PARTS;  // keys of this thread's share
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      if (r < rows) acc[r] *= s_corr[r];
+    }
+#pragma unroll
+    for (int k0 = 0; k0 < KS; k0 += 4) {
+      const int key = part * KS + k0;
+      const float v0 = s_v[key * LD + col], v1 = s_v[(key + 1) * LD + col], v2 = s_v[(key + 2) * LD + col],
+                  v3 = s_v[(key + 3) * LD + col];
+#pragma unroll
+      for (int r = 0; r < kR; ++r) {
+        if (r < rows) {
+          const float4 p4 = *reinterpret_cast<const float4*>(s_p + r * kKT + key);
+          acc[r] = fmaf(p4.x, v0, acc[r]);
+          acc[r] = fmaf(p4.y, v1, acc[r]);
+          acc[r] = fmaf(p4.z, v2, acc[r]);
+          acc[r] = fmaf(p4.w, v3, acc[r]);
+        }
+      }
+    }
+  }
+
+  // add the key shares (in share order), then write
+  const bool direct = a.o_part == nullptr;
+  const int64_t slot = PREFIX ? a.own_splits + split : split;
+  __shared__ float s_l[kR];
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = warp + 8 * i;
+      if (r >= rows) break;
+      s_l[r] = l[i];
+      if (!direct) {
+        const int64_t row = (t.tok0 + r / G) * a.Hq + h * G + r % G;
+        a.ml_part[slot * a.T * a.Hq + row] = make_float2(m[i], l[i]);
+      }
+    }
+  }
+  float* s_o = s_k;  // [PARTS][D], one row at a time
+  for (int r = 0; r < rows; ++r) {
+    __syncthreads();
+    float mine = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kR; ++j)
+      if (j == r) mine = acc[j];
+    s_o[tid] = mine;
+    __syncthreads();
+    if (part == 0) {
+      float o = 0.0f;
+#pragma unroll
+      for (int j = 0; j < PARTS; ++j) o += s_o[j * D + col];
+      const int64_t row = (t.tok0 + r / G) * a.Hq + h * G + r % G;
+      if (direct) store_out(a.out, a.out_dtype, row * D + col, s_l[r] > 0.0f ? o / s_l[r] : 0.0f);
+      else a.o_part[(slot * a.T * a.Hq + row) * D + col] = o;
+    }
+  }
+}
+
+template <typename KV, int D>
+cudaError_t launch_simt_t(const AttendArgs& a, bool prefix, cudaStream_t st) {
+  const int qt = kR / a.G;
+  const int64_t items = prefix ? (a.T + qt - 1) / qt : (a.cu_q != nullptr ? a.T / qt + a.B : a.B);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(items), static_cast<unsigned>(a.Hkv),
+                     static_cast<unsigned>(prefix ? a.prefix_splits : a.own_splits));
+  cfg.blockDim = dim3(kThr);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1] = {pdl_attribute()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = prefix ? cudaLaunchKernelEx(&cfg, attend_simt_kernel<KV, D, true>, a)
+                               : cudaLaunchKernelEx(&cfg, attend_simt_kernel<KV, D, false>, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attend_simt(const AttendArgs& a, int kv_dtype, int D, bool prefix, cudaStream_t st) {
+  if (kv_dtype == ETA_FP8_E4M3) return launch_simt_t<Fp8Raw, 128>(a, prefix, st);
+  if (kv_dtype == ETA_BF16)
+    return D == 128 ? launch_simt_t<Bf16Raw, 128>(a, prefix, st) : launch_simt_t<Bf16Raw, 64>(a, prefix, st);
+  return D == 128 ? launch_simt_t<float, 128>(a, prefix, st) : launch_simt_t<float, 64>(a, prefix, st);
+}
+
+}  // namespace eta

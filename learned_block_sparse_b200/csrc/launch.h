@@ -148,6 +148,40 @@ struct DiagCall {
 };
 cudaError_t launch_screen_diagnostics(const DiagCall& c, cudaStream_t st);
 
+struct AppendCall {
+  eta_shape_t shape;
+  eta_tokens_t in;
+  eta_rope_t rope;
+  void* k;
+  void* v;
+  const int32_t* block_table;  // null: contiguous
+  int num_pages;
+  const int32_t* seq_lens;
+  int64_t n;
+  eta_meta_t meta;
+  int32_t* status;
+};
+cudaError_t launch_append(const AppendCall& c, cudaStream_t st);
+
+struct AttendCall {
+  eta_shape_t shape;
+  eta_queries_t in;
+  float beta;
+  int gate;
+  const void* k;
+  const void* v;
+  const int32_t* block_table;  // null: contiguous
+  int num_pages;
+  const int32_t* seq_lens;
+  int64_t n;
+  int64_t window, sinks;       // a window of n or more and no sinks: causal
+  eta_prefix_t prefix;         // n_tokens 0: none
+  void* ws;                    // workspace: header, then partials
+};
+// Workspace bytes for n_new queries (header and partials), on the current device.
+size_t attend_workspace_bytes(const eta_shape_t& s, int64_t n_new, bool with_prefix);
+cudaError_t launch_attend(const AttendCall& c, cudaStream_t st);
+
 // Largest B*Hkv the decode kernel's on-chip prefix table holds.
 constexpr int kMaxBH = 8192;
 // The workspace starts with a fixed header, the part that must be zero before
