@@ -16,7 +16,7 @@ __global__ void __launch_bounds__(256) attend_merge_kernel(const AttendArgs a) {
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (row >= rows || !token_live(a, row / a.Hq)) return;
-  const int slots = a.own_splits + (a.P > 0 ? a.prefix_splits : 0);
+  const int slots = a.own_splits + a.prefix_splits;
   float M = -INFINITY;
   for (int s = lane; s < slots; s += 32) M = fmaxf(M, a.ml_part[s * rows + row].x);
 #pragma unroll
@@ -39,27 +39,29 @@ __global__ void __launch_bounds__(256) attend_merge_kernel(const AttendArgs a) {
   for (int i = 0; i < V; ++i) store_out(a.out, a.out_dtype, row * D + lane + 32 * i, o[i] * inv);
 }
 
-constexpr int kSimtRows = 16;
+enum Kernel { kSimt, kTile };
 
-// Splits of a pass of `items` tiles so that about `want` thread blocks run.
-int splits_for(int64_t items, int64_t want, int64_t key_tiles) {
-  int64_t s = (want + items - 1) / items;
-  if (s > key_tiles) s = key_tiles;
-  if (s > 128) s = 128;
-  return static_cast<int>(s < 1 ? 1 : s);
-}
-
-struct Plan {
-  int own, prefix;  // splits
+// A pass: its kernel and its splits.
+struct Pass {
+  Kernel kernel;
+  int splits;
 };
 
-Plan plan_of(const eta_shape_t& s, int64_t T, bool single, int64_t own_keys, int64_t P) {
-  const int G = s.n_q_heads / s.n_kv_heads;
-  const int64_t qt = kSimtRows / G, want = 4 * static_cast<int64_t>(device_sm_count());
-  Plan p;
-  const int64_t own_items = single ? s.batch : (T + qt - 1) / qt;
-  p.own = splits_for(own_items * s.n_kv_heads, want, (own_keys + 31) / 32);
-  p.prefix = P > 0 ? splits_for((T + qt - 1) / qt * s.n_kv_heads, want, (P + 31) / 32) : 0;
+int clamp_splits(int64_t s, int64_t most) { return static_cast<int>(s > most ? (most < 1 ? 1 : most) : (s < 1 ? 1 : s)); }
+
+// The pass over `keys` keys of T packed queries (own: in `rows` rows, cu given or
+// one each).
+Pass pass_of(const eta_shape_t& s, int64_t T, bool prefix, bool single, int64_t keys) {
+  const int64_t G = s.n_q_heads / s.n_kv_heads, sms = device_sm_count();
+  Pass p;
+  p.kernel = s.kv_dtype == ETA_BF16 && s.q_dtype == ETA_BF16 && (prefix || !single) ? kTile : kSimt;
+  const int64_t qt = (p.kernel == kTile ? kTileRows : kSimtRows) / G;
+  const int64_t items = (prefix ? (T + qt - 1) / qt : (single ? s.batch : T / qt + s.batch)) * s.n_kv_heads;
+  if (p.kernel == kTile)  // one thread block per SM, in one wave
+    p.splits = clamp_splits(sms / items, prefix ? keys / 128 : keys / 256);
+  else                    // about four thread blocks per SM
+    p.splits = clamp_splits((4 * sms + items - 1) / items, (keys + 31) / 32);
+  if (p.splits > 128) p.splits = 128;
   return p;
 }
 
@@ -67,22 +69,18 @@ size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
 
-// Partial rows (slots x rows) a pass of tiles of R rows can leave for up to T
-// queries: splits <= want / items + 1 and rows <= R x items, so at most
-// R (want + items); without a second pass a pass of `want` tiles or more is never
-// split and leaves none. Non-decreasing in T.
-static int64_t partial_rows(int64_t items, int64_t R, int64_t want, bool second) {
-  if (!second && items > want) items = want;
-  return R * (want + items);
-}
-
+// Partial rows (splits x query rows) the passes of a call of up to T queries can
+// leave: at most R (want + items) with splits <= want / items + 1 and R rows per
+// item (kSimt), at most R want with splits <= want / items (kTile), never below the
+// query rows when there are two passes. A single pass that is not split leaves
+// none. Non-decreasing in T.
 size_t attend_workspace_bytes(const eta_shape_t& s, int64_t T, bool with_prefix) {
-  const int64_t G = s.n_q_heads / s.n_kv_heads, qt = kSimtRows / G, want = 4 * static_cast<int64_t>(device_sm_count());
-  const int64_t tiles = (T + qt - 1) / qt * s.n_kv_heads;
-  int64_t rows = partial_rows(tiles, kSimtRows, want, with_prefix);
-  const int64_t single = partial_rows(T * s.n_kv_heads, G, want, with_prefix);  // one query per row and tile
-  if (single > rows) rows = single;
-  if (with_prefix) rows += partial_rows(tiles, kSimtRows, want, true);
+  const int64_t G = s.n_q_heads / s.n_kv_heads, sms = device_sm_count(), qt = kSimtRows / G;
+  auto most = [](int64_t x, int64_t y) { return x > y ? x : y; };
+  int64_t items = most((T + qt - 1) / qt, T) * s.n_kv_heads;
+  if (!with_prefix && items > 4 * sms) items = 4 * sms;
+  int64_t rows = most(kSimtRows * (4 * sms + items), kTileRows * sms);
+  if (with_prefix) rows = 2 * most(rows, T * s.n_q_heads);
   return kWsHeaderBytes + align256(static_cast<size_t>(rows) * sizeof(float2)) +
          align256(static_cast<size_t>(rows) * s.head_dim * sizeof(float));
 }
@@ -91,10 +89,11 @@ cudaError_t launch_attend(const AttendCall& c, cudaStream_t st) {
   AttendArgs a = make_attend_args(c);
   const int D = c.shape.head_dim;
   const int64_t own_keys = a.sinks + a.window < a.n ? a.sinks + a.window : a.n;
-  const Plan p = plan_of(c.shape, a.T, a.cu_q == nullptr, own_keys, a.P);
-  a.own_splits = p.own;
-  a.prefix_splits = p.prefix;
-  const int slots = p.own + p.prefix;
+  const Pass own = pass_of(c.shape, a.T, false, a.cu_q == nullptr, own_keys);
+  const Pass pre = pass_of(c.shape, a.T, true, false, a.P);
+  a.own_splits = own.splits;
+  a.prefix_splits = a.P > 0 ? pre.splits : 0;
+  const int slots = a.own_splits + a.prefix_splits;
   if (slots > 1) {
     unsigned char* w = static_cast<unsigned char*>(c.ws) + kWsHeaderBytes;
     const size_t rows = static_cast<size_t>(a.T) * a.Hq;
@@ -102,8 +101,12 @@ cudaError_t launch_attend(const AttendCall& c, cudaStream_t st) {
     a.o_part = reinterpret_cast<float*>(w + align256(slots * rows * sizeof(float2)));
   }
   cudaError_t e = cudaSuccess;
-  if (a.P > 0) e = launch_attend_simt(a, c.shape.kv_dtype, D, true, st);
-  if (e == cudaSuccess) e = launch_attend_simt(a, c.shape.kv_dtype, D, false, st);
+  auto launch = [&](const Pass& p, bool prefix) {
+    return p.kernel == kTile ? launch_attend_tile(a, D, prefix, st)
+                             : launch_attend_simt(a, c.shape.kv_dtype, D, prefix, st);
+  };
+  if (a.P > 0) e = launch(pre, true);
+  if (e == cudaSuccess) e = launch(own, false);
   if (e != cudaSuccess || slots == 1) return e;
   return D == 128 ? launch_pdl(attend_merge_kernel<128>, static_cast<unsigned>((a.T * a.Hq + 7) / 8), 256u, 0, st, a)
                   : launch_pdl(attend_merge_kernel<64>, static_cast<unsigned>((a.T * a.Hq + 7) / 8), 256u, 0, st, a);

@@ -19,7 +19,7 @@ namespace eta {
 
 namespace {
 
-constexpr int kThr = 256, kKT = 32, kR = 16;  // threads, keys per tile, rows per tile
+constexpr int kThr = 256, kKT = 32, kR = kSimtRows;  // threads, keys per tile, rows per tile
 
 template <typename KV>
 __device__ __forceinline__ void widen_piece(const uint4& w, float* x) { widen16<KV>(w, x); }

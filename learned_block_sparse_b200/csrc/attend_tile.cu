@@ -1,0 +1,529 @@
+// Attention of new tokens on the 5th-generation tensor cores: tiles of 128 query
+// rows (queries x the G heads of a group) against tiles of 128 keys, bf16 caches
+// and queries. Prompt chunks against their row's cache, and the packed queries of
+// all rows against a shared prefix.
+//
+// One thread block per SM holds two query tiles, so that the matrix pipe works on
+// one while the softmax of the other runs:
+//   warps 0-3, 4-7  softmax of tile 0, 1: thread = row, the row's 128 logits in
+//                   registers, running max and sum in fp32, weights back to TMEM
+//   warp 8          issues the MMAs: S = Q K^T (128 x 128 x D), O += P V
+//   warp 9          TMA loads of K and V tiles into a ring of buffers
+// (warps 10 and 11 only complete the warpgroup that gives its registers away: of the
+// 168 a thread starts with, the softmax threads end with 208 and hold a whole row)
+// TMEM (512 columns): S0, S1 (128 each; P overwrites S), O0, O1 (D each). The
+// accumulators never leave TMEM until the end; when a row's maximum grows by more
+// than 2^8 the row's O is rescaled in place (the weights are relative to the last
+// such maximum, so they stay below 2^8), which after the first tiles is rare.
+//
+// Rounding: the weights meet V as bf16 numbers. With bf16 output that one rounding
+// (half a step, 2^-9 of each weight, signs random) is of the output's own size; with
+// fp32 output a second MMA adds the weights' remainders, also as bf16 numbers, so 16
+// bits of every weight take part. Sums, maxima and accumulators are fp32.
+//
+// Keys that no query of the tile sees (past the row's end, before the window, a
+// page outside the pool) may hold anything in memory. Their logits are replaced by
+// -inf, and their V rows are zeroed in shared memory before the MMA reads them
+// (0 x NaN would reach O).
+//
+// Bound: the matrix pipe and the exponentials are balanced on this machine (a
+// 128 x 128 x 128 pair of MMAs takes 1,024 cycles, its 16,384 exponentials 1,024
+// cycles of the special-function units); long prefixes with few rows are bound by
+// HBM.
+#include <atomic>
+
+#include "attend_common.cuh"
+#include "tcgen05.cuh"
+
+namespace eta {
+
+namespace {
+
+constexpr int kTileThreads = 384;
+constexpr int kTR = 128;  // rows per query tile
+constexpr int kTK = 128;  // keys per key tile
+
+enum { kNoGate = 0, kSigmoid = 1, kHard = 2 };
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// two fp32 -> packed bf16, nearest even (lo in the low half)
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Bits i of word w (keys 32 w + i) with lo <= key < hi.
+__device__ __forceinline__ uint32_t range_bits(int64_t lo, int64_t hi, int w) {
+  const int a = static_cast<int>(max(int64_t{0}, min(int64_t{32}, lo - 32 * w)));
+  const int b = static_cast<int>(max(int64_t{0}, min(int64_t{32}, hi - 32 * w)));
+  if (a >= b) return 0u;
+  return (b == 32 ? 0xffffffffu : (1u << b) - 1u) & ~((1u << a) - 1u);
+}
+
+template <int D>
+struct TileSmem {
+  static constexpr int kBufs = D == 128 ? 5 : 8;              // K or V tiles in the ring
+  static constexpr int kTile = kTK * D * 2;                   // bytes of one
+  static constexpr int kQ = kTR * D * 2;                      // bytes of one query tile
+  static constexpr int kBytes = 2 * kQ + kBufs * kTile + 512; // barriers and flags at the end
+};
+
+template <int D, int GATE, bool HILO>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    attend_tile_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap tmk,
+                       const __grid_constant__ CUtensorMap tmv, const int prefix, const int box_rows,
+                       const int store_rows) {
+  using L = TileSmem<D>;
+  constexpr int NB = L::kBufs;
+  extern __shared__ __align__(1024) unsigned char tile_smem[];
+  unsigned char* s_q = tile_smem;                 // two query tiles
+  unsigned char* s_kv = s_q + 2 * L::kQ;          // the ring: K0 V0 K1 V1 ...
+  uint64_t* s_full = reinterpret_cast<uint64_t*>(s_kv + NB * L::kTile);
+  uint64_t* s_empty = s_full + NB;
+  uint64_t* s_qrdy = s_empty + NB;                // query tiles are in shared memory
+  uint64_t* s_sfull = s_qrdy + 1;                 // [2] logits are in TMEM
+  uint64_t* s_prdy = s_sfull + 2;                 // [2] weights are in TMEM
+  uint64_t* s_ofull = s_prdy + 2;                 // all MMAs are done
+  int* s_abort = reinterpret_cast<int*>(s_ofull + 1);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_abort + 1);
+  uint32_t* s_pages = s_tmem + 1;                 // [8] per key tile (mod 8): 16-key groups whose page exists
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int h = blockIdx.y, split = blockIdx.z;
+  const int splits = prefix ? a.prefix_splits : a.own_splits;
+
+  if (tid == 0) {
+    *s_abort = 0;
+    for (int i = 0; i < NB; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], 1);
+    }
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(&s_sfull[w], 2);
+      mbar_init(&s_prdy[w], 128);
+    }
+    mbar_init(s_qrdy, 256);
+    mbar_init(s_ofull, 1);
+    fence_mbar_init();
+  }
+  grid_dependency_wait();
+  allow_dependent_launch();
+
+  // this thread block's queries and keys
+  const int G = a.G;
+  int g_log2 = 0;
+  while ((1 << g_log2) < G) ++g_log2;
+  const int qt_log2 = 8 - g_log2;  // 256 rows
+  OwnTile t;
+  Visible vis;
+  int64_t tiles, tiles_a = 0;
+  const int item = static_cast<int>(gridDim.x) - 1 - static_cast<int>(blockIdx.x);  // long causal tiles first
+  if (prefix) {
+    t.b = 0;
+    t.tok0 = static_cast<int64_t>(item) << qt_log2;
+    t.nq = static_cast<int>(min(a.T - t.tok0, int64_t{1} << qt_log2));
+    t.p0 = a.P;
+    vis.a1 = vis.b0 = 0;
+    vis.b1 = a.P;
+    tiles = (a.P + kTK - 1) / kTK;
+  } else {
+    if (!own_tile(a, item, qt_log2, tid == 0 && h == 0 && split == 0, t)) return;
+    vis = visible_of(a, t.p0, t.p0 + t.nq - 1);
+    tiles_a = (vis.a1 + kTK - 1) / kTK;
+  }
+  const bool paged = prefix ? a.pblocks != nullptr : a.block_table != nullptr;
+  // key tiles of a paged store start on a block: a tile is then 128 / bs whole pages
+  const int64_t base_b = paged ? vis.b0 & ~static_cast<int64_t>(a.bs - 1) : vis.b0;
+  if (!prefix) tiles = tiles_a + (vis.b1 - base_b + kTK - 1) / kTK;
+  const int64_t u0 = tiles * split / splits;
+  const int n = static_cast<int>(tiles * (split + 1) / splits - u0);  // key tiles of this block
+  const int rows = t.nq << g_log2;
+  const int ntiles = rows > kTR ? 2 : 1;
+
+  // first key of key tile u0 + j, and the keys [v0, v1) of it that some query may see
+  auto bounds = [&](int j, int64_t& s0, int& v0, int& v1) {
+    const int64_t u = u0 + j;
+    int64_t lo, hi;
+    if (u < tiles_a) {
+      s0 = u * kTK;
+      lo = 0;
+      hi = vis.a1;
+    } else {
+      s0 = base_b + (u - tiles_a) * kTK;
+      lo = vis.b0;
+      hi = vis.b1;
+    }
+    v0 = static_cast<int>(max(int64_t{0}, lo - s0));
+    v1 = static_cast<int>(min(int64_t{kTK}, hi - s0));
+  };
+
+  if (warp == 8) tmem_alloc(s_tmem, 512);
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  volatile int* abort_flag = s_abort;
+  int armed = 0;  // uses of the ring whose copies were issued (warp 9)
+
+  // 128 x 88 + 256 x 208 registers: the 384 x 168 of the launch
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 9) {
+      // -------------------------------------------------------------- TMA loads
+      for (int j = 0; j < n; ++j) {
+        int64_t s0;
+        int v0, v1;
+        bounds(j, s0, v0, v1);
+        // lane i: rows of its box; a box without a visible key, or whose page is outside
+        // the pool, reads rows past the store, which arrive as zeros
+        const int boxes = kTK / box_rows;
+        int y = store_rows;
+        if (lane < boxes) {
+          const int k0 = lane * box_rows;
+          if (k0 < v1 && k0 + box_rows > v0) {
+            const int64_t r = prefix ? prefix_row(a, h, s0 + k0) : own_row(a, t.b, h, s0 + k0);
+            if (r >= 0) y = static_cast<int>(r);
+            else atomicExch(a.status, static_cast<int32_t>(ETA_ERR_INVALID_ARG));
+          }
+        }
+        if (paged) {  // which 16-key groups have a page
+          uint32_t groups = 0;
+          if (lane < boxes && y != store_rows) groups = ((1u << (box_rows >> 4)) - 1u) << (lane * (box_rows >> 4));
+          groups = __reduce_or_sync(kFull, groups);
+          if (lane == 0) s_pages[j & 7] = groups;
+        }
+        for (int which = 0; which < 2; ++which) {
+          const int use = 2 * j + which, buf = use % NB, round = use / NB;
+          bool ok = true;
+          if (lane == 0) {
+            ok = (round == 0 || mbar_wait_bounded(&s_empty[buf], (round - 1) & 1, s_abort, a.status)) && !*abort_flag;
+            if (ok) mbar_arrive_expect_tx(&s_full[buf], L::kTile);
+          }
+          if (!__shfl_sync(kFull, ok ? 1 : 0, 0)) {  // a wait ran out: nothing more is armed
+            j = n;
+            break;
+          }
+          ++armed;
+          if (lane < boxes) {
+            unsigned char* dst = s_kv + static_cast<size_t>(buf) * L::kTile + lane * box_rows * 128;
+  #pragma unroll
+            for (int x = 0; x < D / 64; ++x)
+              tma_load_rows(dst + x * kTK * 128, which == 0 ? &tmk : &tmv, x * 64, y, &s_full[buf]);
+          }
+          __syncwarp();
+        }
+      }
+    } else if (warp == 8) {
+      // ------------------------------------------------------------------ MMAs
+      if (lane == 0) {
+        constexpr uint32_t dS = mma_desc_bf16(kTR, kTK, false), dO = mma_desc_bf16(kTR, D, true);
+        const uint32_t q_addr = smem_u32(s_q), kv_addr = smem_u32(s_kv);
+        bool ok = mbar_wait_bounded(s_qrdy, 0, s_abort, a.status);
+        auto wait_use = [&](int use) {
+          return mbar_wait_bounded(&s_full[use % NB], (use / NB) & 1, s_abort, a.status);
+        };
+        auto logits = [&](int w, int j) {  // S_w = Q_w K_j^T
+          const uint32_t k_addr = kv_addr + static_cast<uint32_t>((2 * j) % NB) * L::kTile;
+  #pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t off = (ks >> 2) * kTK * 128 + (ks & 3) * 32;
+            mma_f16_ss(tmem + w * 128, smem_desc(q_addr + w * L::kQ + off, 16, 1024), smem_desc(k_addr + off, 16, 1024),
+                       dS, ks > 0);
+          }
+          tc_commit(&s_sfull[w]);
+          mbar_arrive(&s_sfull[w]);  // also publishes what the loads' barrier published (the page mask)
+        };
+        if (ok) ok = n > 0 && wait_use(0);
+        tc_fence_after();
+        if (ok) {
+          for (int w = 0; w < ntiles; ++w) logits(w, 0);
+          tc_commit(&s_empty[0]);
+        }
+        for (int j = 0; ok && j < n; ++j) {
+          const uint32_t v_addr = kv_addr + static_cast<uint32_t>((2 * j + 1) % NB) * L::kTile;
+          for (int w = 0; w < ntiles; ++w) {
+            ok = mbar_wait_bounded(&s_prdy[w], j & 1, s_abort, a.status) && (w > 0 || wait_use(2 * j + 1));
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t o = tmem + 256 + w * D, p = tmem + w * 128;
+  #pragma unroll
+            for (int ks = 0; ks < kTK / 16; ++ks)
+              mma_f16_ts(o, p + ks * 8, smem_desc(v_addr + ks * 2048, kTK * 128, 1024), dO, j > 0 || ks > 0);
+            if (HILO) {
+  #pragma unroll
+              for (int ks = 0; ks < kTK / 16; ++ks)
+                mma_f16_ts(o, p + 64 + ks * 8, smem_desc(v_addr + ks * 2048, kTK * 128, 1024), dO, true);
+            }
+            if (w == ntiles - 1) tc_commit(&s_empty[(2 * j + 1) % NB]);
+            if (j + 1 < n) {
+              if (w == 0) {
+                ok = wait_use(2 * j + 2);
+                if (!ok) break;
+                tc_fence_after();
+              }
+              logits(w, j + 1);
+              if (w == ntiles - 1) tc_commit(&s_empty[(2 * j + 2) % NB]);
+            }
+          }
+        }
+        tc_commit(s_ofull);  // after the last MMA, or after those issued before an abort
+        if (!ok) {
+          const uint64_t t0 = global_timer_ns();
+          while (!mbar_try_wait(s_ofull, 0) && global_timer_ns() - t0 < kWaitLimitNs) {
+          }
+        }
+      }
+      __syncwarp();
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    // --------------------------------------------------------------- softmax
+    const int w = warp >> 2, r = tid & 127;        // tile, row of the tile
+    const int row = w * kTR + r;                   // row of the block: query row >> g_log2, head row & (G - 1)
+    const bool live = row < rows;
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(warp & 3) << 21);  // lanes 32 (warp % 4) ..
+    const uint32_t sp = lane_addr + w * 128, so = lane_addr + 256 + w * D;
+    const int64_t tok = t.tok0 + (row >> g_log2);
+    const int64_t qrow = tok * a.Hq + h * G + (row & (G - 1));
+    {
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + (live ? qrow : 0) * D);
+      unsigned char* dst = s_q + w * L::kQ;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 x = live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(dst + tile_offset(kTR, r, c)) = x;
+      }
+      fence_async_smem();
+      mbar_arrive(s_qrdy);
+    }
+    const int64_t p = t.p0 + (row >> g_log2);      // this row's position (prefix: past every key)
+    const float c2 = a.qscale * kLog2e;
+    float tau = 0.0f;
+    if (GATE != kNoGate && live) tau = a.tau[tok * a.tau_stride + h * G + (row & (G - 1))];
+    const float gk = -a.beta * kLog2e * a.qscale, gb = a.beta * kLog2e * tau;
+    float m = -INFINITY, l = 0.0f;                 // log2 units
+    bool ok = w < ntiles;
+    for (int j = 0; ok && j < n; ++j) {
+      ok = mbar_wait_bounded(&s_sfull[w], j & 1, s_abort, a.status);
+      ok = __all_sync(kFull, ok);
+      if (!ok) break;
+      tc_fence_after();
+      int64_t s0;
+      int v0, v1;
+      bounds(j, s0, v0, v1);
+      float s[kTK];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tmem_ld32(sp + 32 * i, reinterpret_cast<uint32_t*>(s) + 32 * i);
+      tc_wait_ld();
+      const uint32_t groups = paged ? s_pages[j & 7] : 0xffu;
+      // every key visible to every row of the block and none of them a row's own: no checks
+      const bool inside = v0 == 0 && v1 == kTK && groups == 0xffu &&
+                          (prefix || (s0 + kTK <= t.p0 && (s0 > t.p0 + t.nq - 1 - a.window || s0 + kTK <= a.sinks)));
+      if (GATE == kSigmoid) {
+        const int own = prefix ? -1 : static_cast<int>(min(int64_t{kTK}, p - s0));
+#pragma unroll
+        for (int i = 0; i < kTK; ++i) {
+          const float g = s[i] * c2 * rcp(1.0f + ex2(fmaf(s[i], gk, gb)));
+          s[i] = (!inside && i == own) ? s[i] * c2 : g;
+        }
+      } else if (GATE == kHard) {
+        const int own = prefix ? -1 : static_cast<int>(min(int64_t{kTK}, p - s0));
+#pragma unroll
+        for (int i = 0; i < kTK; ++i) s[i] = (s[i] * a.qscale >= tau || (!inside && i == own)) ? s[i] * c2 : -INFINITY;
+      }
+      if (!inside) {
+        const int64_t up = p - s0 + 1, from = p - a.window + 1 - s0, sk = a.sinks - s0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t see = range_bits(v0, v1, q);
+          if (!prefix) see &= range_bits(0, up, q) & (range_bits(from, kTK, q) | range_bits(0, sk, q));
+          const uint32_t pg = groups >> (2 * q);
+          see &= ((pg & 1u) ? 0xffffu : 0u) | ((pg & 2u) ? 0xffff0000u : 0u);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) s[32 * q + i] = (see >> i) & 1u ? s[32 * q + i] : -INFINITY;
+        }
+        if (w == 0) {
+          // thread r owns key r: its V row is zeroed when no query may see it
+          const bool dead = r < v0 || r >= v1 || !((groups >> (r >> 4)) & 1u);
+          if (__any_sync(kFull, dead)) {
+            const int use = 2 * j + 1;
+            ok = mbar_wait_bounded(&s_full[use % NB], (use / NB) & 1, s_abort, a.status);
+            if (ok && dead) {
+              unsigned char* vt = s_kv + static_cast<size_t>(use % NB) * L::kTile;
+#pragma unroll
+              for (int c = 0; c < D / 8; ++c)
+                *reinterpret_cast<uint4*>(vt + tile_offset(kTK, r, c)) = make_uint4(0u, 0u, 0u, 0u);
+              fence_async_smem();
+            }
+            ok = __all_sync(kFull, ok);
+            if (!ok) break;
+          }
+        }
+      }
+      // running maximum (four chains), in log2 units
+      float m0 = s[0], m1 = s[1], m2 = s[2], m3 = s[3];
+#pragma unroll
+      for (int i = 4; i < kTK; i += 4) {
+        m0 = fmaxf(m0, s[i]);
+        m1 = fmaxf(m1, s[i + 1]);
+        m2 = fmaxf(m2, s[i + 2]);
+        m3 = fmaxf(m3, s[i + 3]);
+      }
+      float mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+      if (GATE == kNoGate) mx *= c2;
+      const bool grow = mx > m + 8.0f;  // (also the first visible key: m is -inf until then)
+      if (__any_sync(kFull, grow)) {
+        const float mn = grow ? mx : m;
+        const float f = m == mn ? 1.0f : ex2(m - mn);
+        l *= f;
+        m = mn;
+        if (j > 0) {
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            float o[32];
+            tmem_ld32(so + 32 * i, reinterpret_cast<uint32_t*>(o));
+            tc_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= f;
+            tmem_st32(so + 32 * i, reinterpret_cast<const uint32_t*>(o));
+          }
+        }
+      }
+      const float base = m == -INFINITY ? 0.0f : m;
+      float l0 = 0.0f, l1 = 0.0f, l2 = 0.0f, l3 = 0.0f;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t hi[32], lo[HILO ? 32 : 1];
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          const int e = 64 * q + 2 * i;
+          float x[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            x[k] = GATE == kNoGate ? ex2(fmaf(s[e + k], c2, -base)) : ex2(s[e + k] - base);
+          l0 += x[0];
+          l1 += x[1];
+          l2 += x[2];
+          l3 += x[3];
+          hi[i] = pack2(x[0], x[1]);
+          hi[i + 1] = pack2(x[2], x[3]);
+          if (HILO) {
+            lo[i] = pack2(x[0] - bf16_lo(hi[i]), x[1] - bf16_hi(hi[i]));
+            lo[i + 1] = pack2(x[2] - bf16_lo(hi[i + 1]), x[3] - bf16_hi(hi[i + 1]));
+          }
+        }
+        tmem_st32(sp + 32 * q, hi);
+        if (HILO) tmem_st32(sp + 64 + 32 * q, lo);
+      }
+      l += (l0 + l1) + (l2 + l3);
+      tc_wait_st();
+      tc_fence_before();
+      mbar_arrive(&s_prdy[w]);
+    }
+    // -------------------------------------------------------------- epilogue
+    if (ok) ok = __all_sync(kFull, mbar_wait_bounded(s_ofull, 0, s_abort, a.status));
+    if (ok) {
+      tc_fence_after();
+      const bool direct = a.o_part == nullptr;
+      const int64_t part = static_cast<int64_t>(prefix ? a.own_splits + split : split) * a.T * a.Hq + qrow;
+      const float inv = direct ? (l > 0.0f ? 1.0f / l : 0.0f) : 1.0f;
+      if (live && !direct) a.ml_part[part] = make_float2(m, l);
+      if (n > 0) {
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          float o[32];
+          tmem_ld32(so + 32 * i, reinterpret_cast<uint32_t*>(o));
+          tc_wait_ld();
+          if (!live) continue;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] *= inv;
+          if (direct && a.out_dtype == ETA_BF16) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + qrow * D + 32 * i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              dst[e] = make_uint4(pack2(o[8 * e], o[8 * e + 1]), pack2(o[8 * e + 2], o[8 * e + 3]),
+                                  pack2(o[8 * e + 4], o[8 * e + 5]), pack2(o[8 * e + 6], o[8 * e + 7]));
+          } else {
+            float4* dst = reinterpret_cast<float4*>(direct ? static_cast<float*>(a.out) + qrow * D + 32 * i
+                                                           : a.o_part + part * D + 32 * i);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+        }
+      }
+      tc_fence_before();
+    }
+  }
+  __syncthreads();
+  if (*abort_flag && warp == 9 && lane == 0) {
+    // an aborted block may have copies in flight: the last use of every buffer lands before it exits
+    for (int use = max(0, armed - NB); use < armed; ++use) {
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(&s_full[use % NB], (use / NB) & 1) && global_timer_ns() - t0 < kWaitLimitNs) {
+      }
+    }
+  }
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_free(tmem, 512);
+  }
+}
+
+template <int D, int GATE, bool HILO>
+cudaError_t launch_tile_t(const AttendArgs& a, dim3 grid, bool prefix, const CUtensorMap& tmk, const CUtensorMap& tmv,
+                          int box_rows, int store_rows, cudaStream_t st) {
+  static std::atomic<uint64_t> smem_done{0};
+  cudaError_t e = allow_max_smem(smem_done, reinterpret_cast<const void*>(attend_tile_kernel<D, GATE, HILO>));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kTileThreads);
+  cfg.dynamicSmemBytes = TileSmem<D>::kBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1] = {pdl_attribute()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, attend_tile_kernel<D, GATE, HILO>, a, tmk, tmv, prefix ? 1 : 0, box_rows, store_rows);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_tile_d(const AttendArgs& a, dim3 grid, bool prefix, const CUtensorMap& tmk, const CUtensorMap& tmv,
+                          int box_rows, int store_rows, cudaStream_t st) {
+  const int gate = a.tau == nullptr ? kNoGate : (a.gate == ETA_GATE_HARD ? kHard : kSigmoid);
+  const bool two = a.out_dtype == ETA_F32;
+#define ETA_TILE(g)                                                                                         \
+  (two ? launch_tile_t<D, g, true>(a, grid, prefix, tmk, tmv, box_rows, store_rows, st)                    \
+       : launch_tile_t<D, g, false>(a, grid, prefix, tmk, tmv, box_rows, store_rows, st))
+  return gate == kNoGate ? ETA_TILE(kNoGate) : (gate == kSigmoid ? ETA_TILE(kSigmoid) : ETA_TILE(kHard));
+#undef ETA_TILE
+}
+
+}  // namespace
+
+cudaError_t launch_attend_tile(const AttendArgs& a, int D, bool prefix, cudaStream_t st) {
+  const bool paged = prefix ? a.pblocks != nullptr : a.block_table != nullptr;
+  const int64_t store = paged ? static_cast<int64_t>(a.num_pages) * a.Hkv * a.bs
+                              : (prefix ? a.Hkv * a.pcap : static_cast<int64_t>(a.B) * a.Hkv * a.cap);
+  const int box_rows = paged ? a.bs : kTK;
+  CUtensorMap tmk, tmv;
+  if (!encode_rows_map(&tmk, prefix ? a.pk : a.k, store, D, 2, box_rows) ||
+      !encode_rows_map(&tmv, prefix ? a.pv : a.v, store, D, 2, box_rows))
+    return cudaErrorInvalidValue;
+  const int64_t qt = kTileRows / a.G;
+  const int64_t items = prefix ? (a.T + qt - 1) / qt : (a.cu_q != nullptr ? a.T / qt + a.B : a.B);
+  const dim3 grid(static_cast<unsigned>(items), static_cast<unsigned>(a.Hkv),
+                  static_cast<unsigned>(prefix ? a.prefix_splits : a.own_splits));
+  return D == 128 ? launch_tile_d<128>(a, grid, prefix, tmk, tmv, box_rows, static_cast<int>(store), st)
+                  : launch_tile_d<64>(a, grid, prefix, tmk, tmv, box_rows, static_cast<int>(store), st);
+}
+
+}  // namespace eta
