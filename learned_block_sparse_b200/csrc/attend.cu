@@ -39,7 +39,9 @@ __global__ void __launch_bounds__(256) attend_merge_kernel(const AttendArgs a) {
   for (int i = 0; i < V; ++i) store_out(a.out, a.out_dtype, row * D + lane + 32 * i, o[i] * inv);
 }
 
-enum Kernel { kSimt, kTile };
+enum Kernel { kSimt, kTile, kRow };
+
+constexpr int kRowWant = 10;  // thread blocks per SM that a kRow pass is split into
 
 // A pass: its kernel and its splits.
 struct Pass {
@@ -54,12 +56,15 @@ int clamp_splits(int64_t s, int64_t most) { return static_cast<int>(s > most ? (
 Pass pass_of(const eta_shape_t& s, int64_t T, bool prefix, bool single, int64_t keys) {
   const int64_t G = s.n_q_heads / s.n_kv_heads, sms = device_sm_count();
   Pass p;
-  p.kernel = s.kv_dtype == ETA_BF16 && s.q_dtype == ETA_BF16 && (prefix || !single) ? kTile : kSimt;
+  const bool bf16 = s.kv_dtype == ETA_BF16 && s.q_dtype == ETA_BF16;
+  p.kernel = !prefix && single && (bf16 || s.kv_dtype == ETA_FP8_E4M3) ? kRow : (bf16 ? kTile : kSimt);
   const int64_t qt = (p.kernel == kTile ? kTileRows : kSimtRows) / G;
   const int64_t items = (prefix ? (T + qt - 1) / qt : (single ? s.batch : T / qt + s.batch)) * s.n_kv_heads;
-  if (p.kernel == kTile)  // one thread block per SM, in one wave
+  if (p.kernel == kTile)       // one thread block per SM, in one wave
     p.splits = clamp_splits(sms / items, prefix ? keys / 128 : keys / 256);
-  else                    // about four thread blocks per SM
+  else if (p.kernel == kRow)   // two thread blocks per SM, five waves (the last one is rarely full); 64 keys at least
+    p.splits = clamp_splits((kRowWant * sms + items - 1) / items, keys / 64);
+  else                         // about four thread blocks per SM
     p.splits = clamp_splits((4 * sms + items - 1) / items, (keys + 31) / 32);
   if (p.splits > 128) p.splits = 128;
   return p;
@@ -71,15 +76,15 @@ size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Partial rows (splits x query rows) the passes of a call of up to T queries can
 // leave: at most R (want + items) with splits <= want / items + 1 and R rows per
-// item (kSimt), at most R want with splits <= want / items (kTile), never below the
+// item (kSimt, kRow: R = G), at most R want with splits <= want / items (kTile), never below the
 // query rows when there are two passes. A single pass that is not split leaves
 // none. Non-decreasing in T.
 size_t attend_workspace_bytes(const eta_shape_t& s, int64_t T, bool with_prefix) {
   const int64_t G = s.n_q_heads / s.n_kv_heads, sms = device_sm_count(), qt = kSimtRows / G;
   auto most = [](int64_t x, int64_t y) { return x > y ? x : y; };
   int64_t items = most((T + qt - 1) / qt, T) * s.n_kv_heads;
-  if (!with_prefix && items > 4 * sms) items = 4 * sms;
-  int64_t rows = most(kSimtRows * (4 * sms + items), kTileRows * sms);
+  if (!with_prefix && items > kRowWant * sms) items = kRowWant * sms;
+  int64_t rows = most(most(kSimtRows * (4 * sms + items), kTileRows * sms), G * (kRowWant * sms + items));
   if (with_prefix) rows = 2 * most(rows, T * s.n_q_heads);
   return kWsHeaderBytes + align256(static_cast<size_t>(rows) * sizeof(float2)) +
          align256(static_cast<size_t>(rows) * s.head_dim * sizeof(float));
@@ -102,8 +107,9 @@ cudaError_t launch_attend(const AttendCall& c, cudaStream_t st) {
   }
   cudaError_t e = cudaSuccess;
   auto launch = [&](const Pass& p, bool prefix) {
-    return p.kernel == kTile ? launch_attend_tile(a, D, prefix, st)
-                             : launch_attend_simt(a, c.shape.kv_dtype, D, prefix, st);
+    if (p.kernel == kTile) return launch_attend_tile(a, D, prefix, st);
+    if (p.kernel == kRow) return launch_attend_row(a, c.shape.kv_dtype, D, st);
+    return launch_attend_simt(a, c.shape.kv_dtype, D, prefix, st);
   };
   if (a.P > 0) e = launch(pre, true);
   if (e == cudaSuccess) e = launch(own, false);

@@ -1,0 +1,532 @@
+// Attention of one new token per row on the warp-level tensor-core instructions
+// (bf16 queries; bf16 or fp8 e4m3 caches): a stream of the row's visible keys, all G
+// heads of a group from one read of K and V.
+//
+// Bound: HBM. G <= 8 query rows are far too few for a 128-row tile, but on the CUDA
+// cores the products of G = 4 heads cost more issue slots than the bytes leave time
+// for; as m16n8k16 tiles (rows 0-7: the heads) they take a tenth of them.
+//
+// One thread block takes one (row, kv head) and a range of its key chunks; its four
+// warps take chunks in turn. Every warp streams for itself: lane 0 arms a barrier and
+// starts the tensor copies of a chunk (8 KB of K and V: 16 keys of bf16 at d = 128,
+// 32 of fp8 or at d = 64) into one of the warp's three buffers, two chunks ahead of the one
+// being attended, so warps never wait for one another before the final merge. Two
+// thread blocks fit per SM (96 KB each): 128 KB in flight.
+//
+// Rounding: the weights' fp32 value is split into two bf16 (f16 with fp8 values)
+// numbers, the first in rows 0-7 of the A operand, the remainder in rows 8-15, so one
+// MMA carries 16 bits of every weight.
+//
+// Keys of a chunk that the token does not see (a chunk's ends, a page outside the
+// pool) may hold anything: their logits become -inf and their V rows are zeroed in
+// shared memory (0 x NaN would reach the output).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "attend_common.cuh"
+#include "tcgen05.cuh"
+
+namespace eta {
+
+namespace {
+
+constexpr int kRowWarps = 4, kRowBufs = 3;
+
+__device__ __forceinline__ void ldm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+// D[16x8] += A[16x16] B[16x8], bf16 or f16 operands
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// D[16x8] += A[16x32] B[32x8], e4m3 operands
+__device__ __forceinline__ void mma_e4m3(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float row_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float row_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// four e4m3 bytes -> two f16 pairs, exact
+__device__ __forceinline__ void widen_e4m3(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Four values below 256 -> e4m3 words with v = hi + lo / 16: eight significant bits,
+// all that a bf16 value has (those under 2^-6 of the largest lose their last ones:
+// at most 2^-21 of it).
+__device__ __forceinline__ void split_e4m3(const float (&v)[4], uint32_t& hi, uint32_t& lo) {
+  hi = e4m3_pair(v[0], v[1]) | (e4m3_pair(v[2], v[3]) << 16);
+  uint32_t a, b;
+  widen_e4m3(hi, a, b);
+  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a));
+  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&b));
+  lo = e4m3_pair((v[0] - x.x) * 16.0f, (v[1] - x.y) * 16.0f) |
+       (e4m3_pair((v[2] - y.x) * 16.0f, (v[3] - y.y) * 16.0f) << 16);
+}
+
+template <int D, bool FP8>
+struct RowChunk {
+  static constexpr int EB = FP8 ? 1 : 2;
+  static constexpr int kKeys = 4096 / (D * EB);       // 16 or 32: 4 KB of K
+  static constexpr int kTile = kKeys * D * EB;
+  static constexpr int kBoxes = D * EB / 128;         // 128-byte column boxes
+};
+
+template <int D, int G, bool FP8>
+__global__ void __launch_bounds__(kRowWarps * 32, 2)
+    attend_row_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap tmk,
+                      const __grid_constant__ CUtensorMap tmv, const int box_rows, const int store_rows) {
+  using C = RowChunk<D, FP8>;
+  constexpr int CH = C::kKeys, NT = CH / 8, KST = D / 16, NDT = D / 8;
+  extern __shared__ __align__(1024) unsigned char row_smem[];
+  unsigned char* tiles = row_smem;  // [warp][buffer][K, V]
+  uint64_t* s_bar = reinterpret_cast<uint64_t*>(row_smem + kRowWarps * kRowBufs * 2 * C::kTile);
+  int* s_abort = reinterpret_cast<int*>(s_bar + kRowWarps * kRowBufs);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int h = blockIdx.y, split = blockIdx.z, splits = a.own_splits;
+  if (tid == 0) {
+    *s_abort = 0;
+    for (int i = 0; i < kRowWarps * kRowBufs; ++i) mbar_init(&s_bar[i], 1);
+    fence_mbar_init();
+  }
+  grid_dependency_wait();
+  allow_dependent_launch();
+  OwnTile t;
+  if (!own_tile(a, blockIdx.x, 0, tid == 0 && h == 0 && split == 0, t)) return;
+  const Visible vis = visible_of(a, t.p0, t.p0);
+  const bool paged = a.block_table != nullptr;
+  const int64_t base_b = paged ? vis.b0 & ~static_cast<int64_t>(max(CH, box_rows) - 1) : vis.b0;
+  const int chunks_a = static_cast<int>((vis.a1 + CH - 1) / CH);
+  const int64_t chunks = chunks_a + (vis.b1 - base_b + CH - 1) / CH;
+  const int64_t c0 = chunks * split / splits, c1 = chunks * (split + 1) / splits;
+  const int n = static_cast<int>((c1 - c0 - warp + kRowWarps - 1) / kRowWarps);  // chunks of this warp (may be <= 0)
+
+  // this warp's j-th chunk: first key, and the keys [v0, v1) of it that are visible
+  auto bounds = [&](int j, int64_t& s0, int& v0, int& v1) {
+    const int64_t u = c0 + warp + static_cast<int64_t>(j) * kRowWarps;
+    int64_t lo, hi;
+    if (u < chunks_a) {
+      s0 = u * CH;
+      lo = 0;
+      hi = vis.a1;
+    } else {
+      s0 = base_b + (u - chunks_a) * CH;
+      lo = vis.b0;
+      hi = vis.b1;
+    }
+    v0 = static_cast<int>(max(int64_t{0}, min(int64_t{CH}, lo - s0)));
+    v1 = static_cast<int>(min(int64_t{CH}, hi - s0));
+  };
+  unsigned char* mine = tiles + warp * kRowBufs * 2 * C::kTile;
+  uint64_t* bar = s_bar + warp * kRowBufs;
+  // The row of lane i's box of the j-th chunk (store_rows, past the store, for a box
+  // without a visible key or page: it arrives as zeros). Whole warp.
+  auto locate = [&](int j) -> int {
+    int y = store_rows;
+    if (j < n) {
+      int64_t s0;
+      int v0, v1;
+      bounds(j, s0, v0, v1);
+      const int k0 = lane * box_rows;
+      if (k0 < v1 && k0 + box_rows > v0) {
+        const int64_t r = own_row(a, t.b, h, s0 + k0);
+        if (r >= 0) y = static_cast<int>(r);
+        else atomicExch(a.status, static_cast<int32_t>(ETA_ERR_INVALID_ARG));
+      }
+    }
+    return y;
+  };
+  auto issue = [&](int j, int y) {
+    if (j >= n) return;
+    uint64_t* b = &bar[j % kRowBufs];
+    if (lane == 0) mbar_arrive_expect_tx(b, 2 * C::kTile);
+    __syncwarp();
+    if (lane * box_rows < CH) {
+      unsigned char* kt = mine + (j % kRowBufs) * 2 * C::kTile + lane * box_rows * 128;
+#pragma unroll
+      for (int x = 0; x < C::kBoxes; ++x) {
+        tma_load_rows(kt + x * CH * 128, &tmk, x * (128 / C::EB), y, b);
+        tma_load_rows(kt + C::kTile + x * CH * 128, &tmv, x * (128 / C::EB), y, b);
+      }
+    }
+  };
+  // page state of a chunk's boxes as a mask of 16-key groups
+  auto groups_of = [&](int y) -> uint32_t {
+    uint32_t g = 0;
+    if (lane * box_rows < CH && y != store_rows) g = ((1u << (box_rows >> 4)) - 1u) << (lane * (box_rows >> 4));
+    return __reduce_or_sync(kFull, g);
+  };
+  __syncthreads();  // barriers are initialised
+  uint32_t groups = 0;  // of the chunk in each buffer, a byte each
+#pragma unroll
+  for (int j = 0; j < kRowBufs - 1; ++j) {
+    const int y = locate(j);
+    groups |= groups_of(y) << (8 * j);
+    issue(j, y);
+  }
+
+  // query fragments: row = lane / 4 (head of the group), q = lane % 4
+  const int row = lane >> 2, qd = lane & 3;
+  const bool live = row < G;
+  const int64_t qrow = t.tok0 * a.Hq + h * G + (live ? row : 0);
+  const uint16_t* qp = static_cast<const uint16_t*>(a.q) + qrow * D;
+  uint32_t qa[FP8 ? 1 : KST][2];
+  uint32_t q8[FP8 ? 4 : 1][4];
+  float scale = a.qscale;
+  if constexpr (FP8) {
+    // this thread's dims of k32 step kk: 32 kk + 4 qd + i, then 16 more; scaled by a
+    // power of two so that the head's largest lies in [128, 256)
+    float x[4][2][4];
+    float amax = 0.0f;
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint2 u = *reinterpret_cast<const uint2*>(qp + 32 * kk + 16 * e + 4 * qd);
+        x[kk][e][0] = bf16_lo(u.x);
+        x[kk][e][1] = bf16_hi(u.x);
+        x[kk][e][2] = bf16_lo(u.y);
+        x[kk][e][3] = bf16_hi(u.y);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (!live) x[kk][e][i] = 0.0f;
+          amax = fmaxf(amax, fabsf(x[kk][e][i]));
+        }
+      }
+    amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
+    const int E = (__float_as_int(amax) >> 23) & 0xff;
+    const int e2 = E == 0 ? 0 : max(-120, min(120, 134 - E));
+    const float up = __int_as_float((127 + e2) << 23);
+    scale *= __int_as_float((127 - e2) << 23);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[kk][e][i] *= up;
+      }
+      split_e4m3(x[kk][0], q8[kk][0], q8[kk][1]);
+      split_e4m3(x[kk][1], q8[kk][2], q8[kk][3]);
+    }
+  } else {
+#pragma unroll
+    for (int kk = 0; kk < KST; ++kk) {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(qp + 16 * kk + 2 * qd);
+      qa[kk][0] = live ? w[0] : 0u;
+      qa[kk][1] = live ? w[4] : 0u;
+    }
+  }
+  const bool gated = a.tau != nullptr;
+  const float tau = gated && live ? a.tau[t.tok0 * a.tau_stride + h * G + row] : 0.0f;
+  const float nbl = -a.beta * kLog2e;
+
+  float o[NDT][4];
+#pragma unroll
+  for (int j = 0; j < NDT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
+  float m = -INFINITY, l = 0.0f;  // log2 units; l: this thread's keys
+  bool ok = true;
+  int issued = min(max(n, 0), kRowBufs - 1);
+
+  for (int j = 0; j < n; ++j) {
+    const int buf = j % kRowBufs;
+    // the next copies first: their buffer was released at the end of the last round
+    {
+      const int y = locate(j + kRowBufs - 1), at = 8 * ((j + kRowBufs - 1) % kRowBufs);
+      groups = (groups & ~(0xffu << at)) | (groups_of(y) << at);
+      issue(j + kRowBufs - 1, y);
+      if (j + kRowBufs - 1 < n) issued = j + kRowBufs;
+    }
+    ok = mbar_wait_bounded(&bar[buf], (j / kRowBufs) & 1, s_abort, a.status);
+    ok = __all_sync(kFull, ok);
+    if (!ok) break;
+    int64_t s0;
+    int v0, v1;
+    bounds(j, s0, v0, v1);
+    const uint32_t grp = paged ? groups >> (8 * buf) : 3u;
+    constexpr uint32_t kAll = (1u << (CH / 16)) - 1u;
+    const bool whole = v0 == 0 && v1 == CH && (grp & kAll) == kAll;
+    unsigned char* ktile = mine + buf * 2 * C::kTile;
+    unsigned char* vtile = ktile + C::kTile;
+    uint32_t see = 0xffffffffu;  // bit i: key i
+    if (!whole) {
+      see = (v1 >= 32 ? 0xffffffffu : (1u << v1) - 1u) & ~(v0 >= 32 ? 0xffffffffu : (1u << v0) - 1u);
+      see &= ((grp & 1u) ? 0xffffu : 0u) | ((grp & 2u) ? 0xffff0000u : 0u);
+      for (int r = 0; r < CH; ++r)
+        if (!((see >> r) & 1u))
+          for (int c = lane; c < D * C::EB / 16; c += 32)
+            *reinterpret_cast<uint4*>(vtile + tile_offset(CH, r, c)) = make_uint4(0u, 0u, 0u, 0u);
+      fence_async_smem();  // before the next copy into this buffer
+      __syncwarp();
+    }
+    const uint32_t kt = smem_u32(ktile), vt = smem_u32(vtile);
+
+    // S = Q K^T: even and odd steps apart (shorter chains)
+    float s[NT][2];
+    {
+      float sa[NT][4], sb[NT][4];
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sa[i][e] = sb[i][e] = 0.0f;
+      if constexpr (FP8) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            uint32_t b[4];
+            ldm4(kt + tile_offset(CH, 8 * i + (lane & 7), 4 * u + (lane >> 3)), b);
+            mma_e4m3(sa[i], q8[2 * u], b[0], b[1]);
+            mma_e4m3(sb[i], q8[2 * u + 1], b[2], b[3]);
+          }
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            s[i][e] = fmaf(sa[i][2 + e] + sb[i][2 + e], 0.0625f, sa[i][e] + sb[i][e]) * scale;
+      } else {
+#pragma unroll
+        for (int u = 0; u < KST / 2; ++u)
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            uint32_t b[4];
+            ldm4(kt + tile_offset(CH, 8 * i + (lane & 7), 4 * u + (lane >> 3)), b);
+            mma_bf16(sa[i], qa[2 * u][0], 0u, qa[2 * u][1], 0u, b[0], b[1]);
+            mma_bf16(sb[i], qa[2 * u + 1][0], 0u, qa[2 * u + 1][1], 0u, b[2], b[3]);
+          }
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) s[i][e] = (sa[i][e] + sb[i][e]) * scale;
+      }
+    }
+    // gate, mask, running maximum of this thread's row
+    float bm = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int key = 8 * i + 2 * qd + e;
+        float g = s[i][e] * kLog2e;
+        if (gated && s0 + key != t.p0) {
+          if (a.gate == ETA_GATE_HARD) g = s[i][e] >= tau ? g : -INFINITY;
+          else g *= row_rcp(1.0f + row_ex2(nbl * (s[i][e] - tau)));
+        }
+        if (!((see >> key) & 1u)) g = -INFINITY;
+        s[i][e] = g;
+        bm = fmaxf(bm, g);
+      }
+    bm = fmaxf(bm, __shfl_xor_sync(kFull, bm, 1));
+    bm = fmaxf(bm, __shfl_xor_sync(kFull, bm, 2));
+    const float mn = fmaxf(m, bm);
+    const float base = mn == -INFINITY ? 0.0f : mn;
+    const float corr = mn == -INFINITY ? 1.0f : row_ex2(m - mn);
+    m = mn;
+    float ps = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        s[i][e] = row_ex2(s[i][e] - base);
+        ps += s[i][e];
+      }
+    l = fmaf(l, corr, ps);
+    if (__any_sync(kFull, corr != 1.0f)) {
+#pragma unroll
+      for (int i = 0; i < NDT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][e] *= corr;
+    }
+    // O += P V; weights in two parts
+#pragma unroll
+    for (int m2 = 0; m2 < NT / 2; ++m2) {
+      const int vrow = 16 * m2 + 8 * ((lane >> 3) & 1) + (lane & 7);
+      const float p0 = s[2 * m2][0], p1 = s[2 * m2][1], p2 = s[2 * m2 + 1][0], p3 = s[2 * m2 + 1][1];
+      if constexpr (FP8) {
+        auto pack = [](float x, float y) {
+          const __half2 v = __floats2half2_rn(x, y);
+          return *reinterpret_cast<const uint32_t*>(&v);
+        };
+        const uint32_t h0 = pack(p0, p1), h1 = pack(p2, p3);
+        const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
+        const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+        const uint32_t l0 = pack(p0 - f0.x, p1 - f0.y), l1 = pack(p2 - f1.x, p3 - f1.y);
+#pragma unroll
+        for (int g = 0; g < D / 16; g += 2) {
+          uint32_t r[4], ev[4], od[4];
+          ldm4_t(vt + tile_offset(CH, vrow, g + (lane >> 4)), r);
+          // a register holds two keys x two dims: bytes 0, 2 are the even dim's keys, 1, 3 the odd's
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t w = __byte_perm(r[i], 0u, 0x3120);
+            widen_e4m3(w, ev[i], od[i]);
+          }
+          mma_f16(o[2 * g], h0, l0, h1, l1, ev[0], ev[1]);
+          mma_f16(o[2 * g + 1], h0, l0, h1, l1, od[0], od[1]);
+          mma_f16(o[2 * g + 2], h0, l0, h1, l1, ev[2], ev[3]);
+          mma_f16(o[2 * g + 3], h0, l0, h1, l1, od[2], od[3]);
+        }
+      } else {
+        auto pack = [](float x, float y) {
+          const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+          return *reinterpret_cast<const uint32_t*>(&v);
+        };
+        const uint32_t h0 = pack(p0, p1), h1 = pack(p2, p3);
+        const uint32_t l0 = pack(p0 - bf16_lo(h0), p1 - bf16_hi(h0)), l1 = pack(p2 - bf16_lo(h1), p3 - bf16_hi(h1));
+#pragma unroll
+        for (int jd = 0; jd < NDT; jd += 2) {
+          uint32_t r[4];
+          ldm4_t(vt + tile_offset(CH, vrow, jd + (lane >> 4)), r);
+          mma_bf16(o[jd], h0, l0, h1, l1, r[0], r[1]);
+          mma_bf16(o[jd + 1], h0, l0, h1, l1, r[2], r[3]);
+        }
+      }
+    }
+    __syncwarp();  // every lane is done with the buffer
+  }
+  if (!ok && lane == 0) {  // copies in flight land before the block exits
+    for (int j = max(0, issued - kRowBufs); j < issued; ++j) {
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(&bar[j % kRowBufs], (j / kRowBufs) & 1) && global_timer_ns() - t0 < kWaitLimitNs) {
+      }
+    }
+  }
+
+  // merge the warps: states to shared memory (the buffers are free), warps added in order
+  l += __shfl_xor_sync(kFull, l, 1);
+  l += __shfl_xor_sync(kFull, l, 2);
+  __syncthreads();
+  float* s_o = reinterpret_cast<float*>(row_smem);   // [warp][G][D]
+  float* s_ml = s_o + kRowWarps * G * D;             // [warp][G][2]
+  if (live) {
+#pragma unroll
+    for (int i = 0; i < NDT; ++i) {
+      float* dst = s_o + (warp * G + row) * D;
+      const float x = o[i][0] + o[i][2], y = o[i][1] + o[i][3];
+      if constexpr (FP8) {  // tile 2g + p holds dims 16 g + 2 c + p
+        const int at = 16 * (i >> 1) + (i & 1) + 4 * qd;
+        dst[at] = x;
+        dst[at + 2] = y;
+      } else {
+        *reinterpret_cast<float2*>(dst + 8 * i + 2 * qd) = make_float2(x, y);
+      }
+    }
+    if (qd == 0) {
+      s_ml[(warp * G + row) * 2] = m;
+      s_ml[(warp * G + row) * 2 + 1] = l;
+    }
+  }
+  __syncthreads();
+  if (*reinterpret_cast<volatile int*>(s_abort)) return;
+  const bool direct = a.o_part == nullptr;
+  for (int idx = tid; idx < G * D; idx += kRowWarps * 32) {
+    const int g = idx / D, e = idx % D;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kRowWarps; ++w) M = fmaxf(M, s_ml[(w * G + g) * 2]);
+    float ov = 0.0f, L = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kRowWarps; ++w) {
+      const float c = M == -INFINITY ? 0.0f : exp2f(s_ml[(w * G + g) * 2] - M);
+      ov = fmaf(c, s_o[(w * G + g) * D + e], ov);
+      L = fmaf(c, s_ml[(w * G + g) * 2 + 1], L);
+    }
+    const int64_t out_row = t.tok0 * a.Hq + h * G + g;
+    if (direct) {
+      store_out(a.out, a.out_dtype, out_row * D + e, L > 0.0f ? ov / L : 0.0f);
+    } else {
+      const int64_t part = static_cast<int64_t>(split) * a.T * a.Hq + out_row;
+      a.o_part[part * D + e] = ov;
+      if (e == 0) a.ml_part[part] = make_float2(M, L);
+    }
+  }
+}
+
+template <int D, int G, bool FP8>
+cudaError_t launch_row_t(const AttendArgs& a, const CUtensorMap& tmk, const CUtensorMap& tmv, int box_rows,
+                         int store_rows, cudaStream_t st) {
+  using C = RowChunk<D, FP8>;
+  static std::atomic<uint64_t> smem_done{0};
+  cudaError_t e = allow_max_smem(smem_done, reinterpret_cast<const void*>(attend_row_kernel<D, G, FP8>));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.B), static_cast<unsigned>(a.Hkv), static_cast<unsigned>(a.own_splits));
+  cfg.blockDim = dim3(kRowWarps * 32);
+  cfg.dynamicSmemBytes = kRowWarps * kRowBufs * 2 * C::kTile + 256;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1] = {pdl_attribute()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, attend_row_kernel<D, G, FP8>, a, tmk, tmv, box_rows, store_rows);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int D, bool FP8>
+cudaError_t launch_row_g(const AttendArgs& a, const CUtensorMap& tmk, const CUtensorMap& tmv, int box_rows,
+                         int store_rows, cudaStream_t st) {
+  switch (a.G) {
+    case 1: return launch_row_t<D, 1, FP8>(a, tmk, tmv, box_rows, store_rows, st);
+    case 2: return launch_row_t<D, 2, FP8>(a, tmk, tmv, box_rows, store_rows, st);
+    case 4: return launch_row_t<D, 4, FP8>(a, tmk, tmv, box_rows, store_rows, st);
+    default: return launch_row_t<D, 8, FP8>(a, tmk, tmv, box_rows, store_rows, st);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_attend_row(const AttendArgs& a, int kv_dtype, int D, cudaStream_t st) {
+  const bool fp8 = kv_dtype == ETA_FP8_E4M3;
+  const int CH = 4096 / (D * (fp8 ? 1 : 2));
+  const int box_rows = a.block_table != nullptr && a.bs < CH ? a.bs : CH;
+  const int64_t store = a.block_table != nullptr ? static_cast<int64_t>(a.num_pages) * a.Hkv * a.bs
+                                                 : static_cast<int64_t>(a.B) * a.Hkv * a.cap;
+  CUtensorMap tmk, tmv;
+  if (!encode_rows_map(&tmk, a.k, store, D, fp8 ? 1 : 2, box_rows) ||
+      !encode_rows_map(&tmv, a.v, store, D, fp8 ? 1 : 2, box_rows))
+    return cudaErrorInvalidValue;
+  if (fp8) return launch_row_g<128, true>(a, tmk, tmv, box_rows, static_cast<int>(store), st);
+  return D == 128 ? launch_row_g<128, false>(a, tmk, tmv, box_rows, static_cast<int>(store), st)
+                  : launch_row_g<64, false>(a, tmk, tmv, box_rows, static_cast<int>(store), st);
+}
+
+}  // namespace eta
