@@ -56,8 +56,8 @@ int clamp_splits(int64_t s, int64_t most) { return static_cast<int>(s > most ? (
 Pass pass_of(const eta_shape_t& s, int64_t T, bool prefix, bool single, int64_t keys) {
   const int64_t G = s.n_q_heads / s.n_kv_heads, sms = device_sm_count();
   Pass p;
-  const bool bf16 = s.kv_dtype == ETA_BF16 && s.q_dtype == ETA_BF16;
-  p.kernel = !prefix && single && (bf16 || s.kv_dtype == ETA_FP8_E4M3) ? kRow : (bf16 ? kTile : kSimt);
+  const bool mma = s.kv_dtype == ETA_FP8_E4M3 || (s.kv_dtype == ETA_BF16 && s.q_dtype == ETA_BF16);
+  p.kernel = !mma ? kSimt : (!prefix && single ? kRow : kTile);
   const int64_t qt = (p.kernel == kTile ? kTileRows : kSimtRows) / G;
   const int64_t items = (prefix ? (T + qt - 1) / qt : (single ? s.batch : T / qt + s.batch)) * s.n_kv_heads;
   if (p.kernel == kTile)       // one thread block per SM, in one wave
@@ -107,7 +107,7 @@ cudaError_t launch_attend(const AttendCall& c, cudaStream_t st) {
   }
   cudaError_t e = cudaSuccess;
   auto launch = [&](const Pass& p, bool prefix) {
-    if (p.kernel == kTile) return launch_attend_tile(a, D, prefix, st);
+    if (p.kernel == kTile) return launch_attend_tile(a, c.shape.kv_dtype, D, prefix, st);
     if (p.kernel == kRow) return launch_attend_row(a, c.shape.kv_dtype, D, st);
     return launch_attend_simt(a, c.shape.kv_dtype, D, prefix, st);
   };

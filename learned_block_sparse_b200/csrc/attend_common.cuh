@@ -190,7 +190,7 @@ inline AttendArgs make_attend_args(const AttendCall& c) {
 
 // The passes, one launch each (grids from the arguments).
 cudaError_t launch_attend_simt(const AttendArgs& a, int kv_dtype, int D, bool prefix, cudaStream_t st);
-cudaError_t launch_attend_tile(const AttendArgs& a, int D, bool prefix, cudaStream_t st);
+cudaError_t launch_attend_tile(const AttendArgs& a, int kv_dtype, int D, bool prefix, cudaStream_t st);
 cudaError_t launch_attend_row(const AttendArgs& a, int kv_dtype, int D, cudaStream_t st);  // own pass, one token per row
 constexpr int kSimtRows = 16;   // query rows per thread block of attend_simt_kernel
 constexpr int kTileRows = 256;  // of attend_tile_kernel

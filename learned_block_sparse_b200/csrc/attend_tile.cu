@@ -9,8 +9,9 @@
 //                   registers, running max and sum in fp32, weights back to TMEM
 //   warp 8          issues the MMAs: S = Q K^T (128 x 128 x D), O += P V
 //   warp 9          TMA loads of K and V tiles into a ring of buffers
-// (warps 10 and 11 only complete the warpgroup that gives its registers away: of the
-// 168 a thread starts with, the softmax threads end with 208 and hold a whole row)
+//   warps 10, 11    fp8 caches: widen the tiles to bf16; else nothing
+// (warps 8-11 give registers away: of the 168 a thread starts with, the softmax threads
+// end with 208 and hold a whole row)
 // TMEM (512 columns): S0, S1 (128 each; P overwrites S), O0, O1 (D each). The
 // accumulators never leave TMEM until the end; when a row's maximum grows by more
 // than 2^8 the row's O is rescaled in place (the weights are relative to the last
@@ -30,6 +31,13 @@
 // 128 x 128 x 128 pair of MMAs takes 1,024 cycles, its 16,384 exponentials 1,024
 // cycles of the special-function units); long prefixes with few rows are bound by
 // HBM.
+//
+// fp8 (e4m3) caches: the tiles arrive as bytes and warps 10 and 11 widen them to bf16,
+// exactly, into the ring the MMAs read. (f16 would take a third of the conversions, but
+// its weights end at 2^-24 of the largest, and a value that is zero where the largest
+// weight stands then shows the loss.)
+#include <cuda_fp16.h>
+
 #include <atomic>
 
 #include "attend_common.cuh"
@@ -62,6 +70,19 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return r;
 }
 
+// four e4m3 bytes -> two bf16 pairs, exact (through f16 and fp32)
+__device__ __forceinline__ void e4m3_to_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  uint32_t a, b;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(a), "=r"(b)
+      : "r"(w));
+  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a));
+  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&b));
+  lo = pack2(x.x, x.y);
+  hi = pack2(y.x, y.y);
+}
+
 // Bits i of word w (keys 32 w + i) with lo <= key < hi.
 __device__ __forceinline__ uint32_t range_bits(int64_t lo, int64_t hi, int w) {
   const int a = static_cast<int>(max(int64_t{0}, min(int64_t{32}, lo - 32 * w)));
@@ -70,25 +91,30 @@ __device__ __forceinline__ uint32_t range_bits(int64_t lo, int64_t hi, int w) {
   return (b == 32 ? 0xffffffffu : (1u << b) - 1u) & ~((1u << a) - 1u);
 }
 
-template <int D>
+template <int D, bool FP8>
 struct TileSmem {
-  static constexpr int kBufs = D == 128 ? 5 : 8;              // K or V tiles in the ring
+  static constexpr int kBufs = FP8 ? 3 : (D == 128 ? 5 : 8);  // 16-bit K or V tiles in the ring
   static constexpr int kTile = kTK * D * 2;                   // bytes of one
+  static constexpr int kRawBufs = FP8 ? 4 : 0;                // fp8 tiles as they arrive
+  static constexpr int kRaw = kTK * D;
   static constexpr int kQ = kTR * D * 2;                      // bytes of one query tile
-  static constexpr int kBytes = 2 * kQ + kBufs * kTile + 512; // barriers and flags at the end
+  static constexpr int kBytes = 2 * kQ + kBufs * kTile + kRawBufs * kRaw + 512;  // barriers and flags at the end
 };
 
-template <int D, int GATE, bool HILO>
+template <int D, int GATE, bool HILO, bool FP8>
 __global__ void __launch_bounds__(kTileThreads, 1)
     attend_tile_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap tmk,
                        const __grid_constant__ CUtensorMap tmv, const int prefix, const int box_rows,
                        const int store_rows) {
-  using L = TileSmem<D>;
-  constexpr int NB = L::kBufs;
+  using L = TileSmem<D, FP8>;
+  constexpr int NB = L::kBufs;                    // the ring the MMAs read
+  constexpr int NR = FP8 ? L::kRawBufs : NB;      // the ring the copies fill
+  constexpr int kCopy = FP8 ? L::kRaw : L::kTile;
   extern __shared__ __align__(1024) unsigned char tile_smem[];
   unsigned char* s_q = tile_smem;                 // two query tiles
   unsigned char* s_kv = s_q + 2 * L::kQ;          // the ring: K0 V0 K1 V1 ...
-  uint64_t* s_full = reinterpret_cast<uint64_t*>(s_kv + NB * L::kTile);
+  unsigned char* s_raw = FP8 ? s_kv + NB * L::kTile : s_kv;  // where the copies land
+  uint64_t* s_full = reinterpret_cast<uint64_t*>(s_kv + NB * L::kTile + L::kRawBufs * L::kRaw);
   uint64_t* s_empty = s_full + NB;
   uint64_t* s_qrdy = s_empty + NB;                // query tiles are in shared memory
   uint64_t* s_sfull = s_qrdy + 1;                 // [2] logits are in TMEM
@@ -97,6 +123,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   int* s_abort = reinterpret_cast<int*>(s_ofull + 1);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_abort + 1);
   uint32_t* s_pages = s_tmem + 1;                 // [8] per key tile (mod 8): 16-key groups whose page exists
+  uint64_t* s_rfull = FP8 ? s_ofull + 8 : s_full;   // raw fp8 tiles: landed, converted
+  uint64_t* s_rempty = FP8 ? s_rfull + NR : s_empty;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.y, split = blockIdx.z;
   const int splits = prefix ? a.prefix_splits : a.own_splits;
@@ -104,8 +132,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (tid == 0) {
     *s_abort = 0;
     for (int i = 0; i < NB; ++i) {
-      mbar_init(&s_full[i], 1);
+      mbar_init(&s_full[i], FP8 ? 2 : 1);  // one arrival per converting warp
       mbar_init(&s_empty[i], 1);
+    }
+    for (int i = 0; FP8 && i < NR; ++i) {
+      mbar_init(&s_rfull[i], 1);
+      mbar_init(&s_rempty[i], 2);
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(&s_sfull[w], 2);
@@ -201,11 +233,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (lane == 0) s_pages[j & 7] = groups;
         }
         for (int which = 0; which < 2; ++which) {
-          const int use = 2 * j + which, buf = use % NB, round = use / NB;
+          const int use = 2 * j + which, buf = use % NR, round = use / NR;
           bool ok = true;
           if (lane == 0) {
-            ok = (round == 0 || mbar_wait_bounded(&s_empty[buf], (round - 1) & 1, s_abort, a.status)) && !*abort_flag;
-            if (ok) mbar_arrive_expect_tx(&s_full[buf], L::kTile);
+            ok = (round == 0 || mbar_wait_bounded(&s_rempty[buf], (round - 1) & 1, s_abort, a.status)) && !*abort_flag;
+            if (ok) mbar_arrive_expect_tx(&s_rfull[buf], kCopy);
           }
           if (!__shfl_sync(kFull, ok ? 1 : 0, 0)) {  // a wait ran out: nothing more is armed
             j = n;
@@ -213,10 +245,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
           ++armed;
           if (lane < boxes) {
-            unsigned char* dst = s_kv + static_cast<size_t>(buf) * L::kTile + lane * box_rows * 128;
-  #pragma unroll
-            for (int x = 0; x < D / 64; ++x)
-              tma_load_rows(dst + x * kTK * 128, which == 0 ? &tmk : &tmv, x * 64, y, &s_full[buf]);
+            unsigned char* dst = s_raw + static_cast<size_t>(buf) * kCopy + lane * box_rows * 128;
+#pragma unroll
+            for (int x = 0; x < (FP8 ? 1 : D / 64); ++x)
+              tma_load_rows(dst + x * kTK * 128, which == 0 ? &tmk : &tmv, x * 64, y, &s_rfull[buf]);
           }
           __syncwarp();
         }
@@ -232,7 +264,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         };
         auto logits = [&](int w, int j) {  // S_w = Q_w K_j^T
           const uint32_t k_addr = kv_addr + static_cast<uint32_t>((2 * j) % NB) * L::kTile;
-  #pragma unroll
+#pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             const uint32_t off = (ks >> 2) * kTK * 128 + (ks & 3) * 32;
             mma_f16_ss(tmem + w * 128, smem_desc(q_addr + w * L::kQ + off, 16, 1024), smem_desc(k_addr + off, 16, 1024),
@@ -254,11 +286,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if (!ok) break;
             tc_fence_after();
             const uint32_t o = tmem + 256 + w * D, p = tmem + w * 128;
-  #pragma unroll
+#pragma unroll
             for (int ks = 0; ks < kTK / 16; ++ks)
               mma_f16_ts(o, p + ks * 8, smem_desc(v_addr + ks * 2048, kTK * 128, 1024), dO, j > 0 || ks > 0);
             if (HILO) {
-  #pragma unroll
+#pragma unroll
               for (int ks = 0; ks < kTK / 16; ++ks)
                 mma_f16_ts(o, p + 64 + ks * 8, smem_desc(v_addr + ks * 2048, kTK * 128, 1024), dO, true);
             }
@@ -282,6 +314,44 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
       }
       __syncwarp();
+    } else if (FP8) {
+      // ------------------------------------- fp8 tiles to bf16 (warps 10, 11)
+      // A thread widens 16-byte pieces (16 keys or values of one row) of every second
+      // group of 32; V rows that no query may see become zeros here.
+      bool ok = true;
+      for (int use = 0; ok && use < 2 * n; ++use) {
+        const int raw = use % NR, buf = use % NB, round = use / NB;
+        ok = mbar_wait_bounded(&s_rfull[raw], (use / NR) & 1, s_abort, a.status) &&
+             (round == 0 || mbar_wait_bounded(&s_empty[buf], (round - 1) & 1, s_abort, a.status));
+        ok = __all_sync(kFull, ok);
+        if (!ok) break;
+        int64_t s0;
+        int v0, v1;
+        bounds(use >> 1, s0, v0, v1);
+        const uint32_t groups = paged ? s_pages[(use >> 1) & 7] : 0xffu;
+        const unsigned char* src = s_raw + static_cast<size_t>(raw) * kCopy;
+        unsigned char* dst = s_kv + static_cast<size_t>(buf) * L::kTile;
+#pragma unroll 4
+        for (int i = 0; i < kTK * 8 / 64; ++i) {
+          const int at = (warp & 1) * 32 + i * 64;           // 32 pieces: rows of one column of pieces
+          const int r = (at & 127) + lane, c = at >> 7;
+          const uint4 x = *reinterpret_cast<const uint4*>(src + tile_offset(kTK, r, c));
+          uint4 lo, hi;
+          e4m3_to_bf16(x.x, lo.x, lo.y);
+          e4m3_to_bf16(x.y, lo.z, lo.w);
+          e4m3_to_bf16(x.z, hi.x, hi.y);
+          e4m3_to_bf16(x.w, hi.z, hi.w);
+          if ((use & 1) && (r < v0 || r >= v1 || !((groups >> (r >> 4)) & 1u))) lo = hi = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(dst + tile_offset(kTK, r, 2 * c)) = lo;
+          *reinterpret_cast<uint4*>(dst + tile_offset(kTK, r, 2 * c + 1)) = hi;
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&s_full[buf]);
+          mbar_arrive(&s_rempty[raw]);
+        }
+      }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
@@ -293,6 +363,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t sp = lane_addr + w * 128, so = lane_addr + 256 + w * D;
     const int64_t tok = t.tok0 + (row >> g_log2);
     const int64_t qrow = tok * a.Hq + h * G + (row & (G - 1));
+    const float qs = a.qscale;                     // logit = S qs
     {
       const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + (live ? qrow : 0) * D);
       unsigned char* dst = s_q + w * L::kQ;
@@ -305,10 +376,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       mbar_arrive(s_qrdy);
     }
     const int64_t p = t.p0 + (row >> g_log2);      // this row's position (prefix: past every key)
-    const float c2 = a.qscale * kLog2e;
+    const float c2 = qs * kLog2e;
     float tau = 0.0f;
     if (GATE != kNoGate && live) tau = a.tau[tok * a.tau_stride + h * G + (row & (G - 1))];
-    const float gk = -a.beta * kLog2e * a.qscale, gb = a.beta * kLog2e * tau;
+    const float gk = -a.beta * kLog2e * qs, gb = a.beta * kLog2e * tau;
     float m = -INFINITY, l = 0.0f;                 // log2 units
     bool ok = w < ntiles;
     for (int j = 0; ok && j < n; ++j) {
@@ -337,7 +408,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       } else if (GATE == kHard) {
         const int own = prefix ? -1 : static_cast<int>(min(int64_t{kTK}, p - s0));
 #pragma unroll
-        for (int i = 0; i < kTK; ++i) s[i] = (s[i] * a.qscale >= tau || (!inside && i == own)) ? s[i] * c2 : -INFINITY;
+        for (int i = 0; i < kTK; ++i) s[i] = (s[i] * qs >= tau || (!inside && i == own)) ? s[i] * c2 : -INFINITY;
       }
       if (!inside) {
         const int64_t up = p - s0 + 1, from = p - a.window + 1 - s0, sk = a.sinks - s0;
@@ -350,7 +421,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) s[32 * q + i] = (see >> i) & 1u ? s[32 * q + i] : -INFINITY;
         }
-        if (w == 0) {
+        if (!FP8 && w == 0) {
           // thread r owns key r: its V row is zeroed when no query may see it
           const bool dead = r < v0 || r >= v1 || !((groups >> (r >> 4)) & 1u);
           if (__any_sync(kFull, dead)) {
@@ -465,9 +536,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   __syncthreads();
   if (*abort_flag && warp == 9 && lane == 0) {
     // an aborted block may have copies in flight: the last use of every buffer lands before it exits
-    for (int use = max(0, armed - NB); use < armed; ++use) {
+    for (int use = max(0, armed - NR); use < armed; ++use) {
       const uint64_t t0 = global_timer_ns();
-      while (!mbar_try_wait(&s_full[use % NB], (use / NB) & 1) && global_timer_ns() - t0 < kWaitLimitNs) {
+      while (!mbar_try_wait(&s_rfull[use % NR], (use / NR) & 1) && global_timer_ns() - t0 < kWaitLimitNs) {
       }
     }
   }
@@ -477,53 +548,56 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   }
 }
 
-template <int D, int GATE, bool HILO>
+template <int D, int GATE, bool HILO, bool FP8>
 cudaError_t launch_tile_t(const AttendArgs& a, dim3 grid, bool prefix, const CUtensorMap& tmk, const CUtensorMap& tmv,
                           int box_rows, int store_rows, cudaStream_t st) {
   static std::atomic<uint64_t> smem_done{0};
-  cudaError_t e = allow_max_smem(smem_done, reinterpret_cast<const void*>(attend_tile_kernel<D, GATE, HILO>));
+  cudaError_t e = allow_max_smem(smem_done, reinterpret_cast<const void*>(attend_tile_kernel<D, GATE, HILO, FP8>));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(kTileThreads);
-  cfg.dynamicSmemBytes = TileSmem<D>::kBytes;
+  cfg.dynamicSmemBytes = TileSmem<D, FP8>::kBytes;
   cfg.stream = st;
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, attend_tile_kernel<D, GATE, HILO>, a, tmk, tmv, prefix ? 1 : 0, box_rows, store_rows);
+  e = cudaLaunchKernelEx(&cfg, attend_tile_kernel<D, GATE, HILO, FP8>, a, tmk, tmv, prefix ? 1 : 0, box_rows, store_rows);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <int D>
+template <int D, bool FP8>
 cudaError_t launch_tile_d(const AttendArgs& a, dim3 grid, bool prefix, const CUtensorMap& tmk, const CUtensorMap& tmv,
                           int box_rows, int store_rows, cudaStream_t st) {
   const int gate = a.tau == nullptr ? kNoGate : (a.gate == ETA_GATE_HARD ? kHard : kSigmoid);
   const bool two = a.out_dtype == ETA_F32;
 #define ETA_TILE(g)                                                                                         \
-  (two ? launch_tile_t<D, g, true>(a, grid, prefix, tmk, tmv, box_rows, store_rows, st)                    \
-       : launch_tile_t<D, g, false>(a, grid, prefix, tmk, tmv, box_rows, store_rows, st))
+  (two ? launch_tile_t<D, g, true, FP8>(a, grid, prefix, tmk, tmv, box_rows, store_rows, st)               \
+       : launch_tile_t<D, g, false, FP8>(a, grid, prefix, tmk, tmv, box_rows, store_rows, st))
   return gate == kNoGate ? ETA_TILE(kNoGate) : (gate == kSigmoid ? ETA_TILE(kSigmoid) : ETA_TILE(kHard));
 #undef ETA_TILE
 }
 
 }  // namespace
 
-cudaError_t launch_attend_tile(const AttendArgs& a, int D, bool prefix, cudaStream_t st) {
+cudaError_t launch_attend_tile(const AttendArgs& a, int kv_dtype, int D, bool prefix, cudaStream_t st) {
+  const bool fp8 = kv_dtype == ETA_FP8_E4M3;
   const bool paged = prefix ? a.pblocks != nullptr : a.block_table != nullptr;
   const int64_t store = paged ? static_cast<int64_t>(a.num_pages) * a.Hkv * a.bs
                               : (prefix ? a.Hkv * a.pcap : static_cast<int64_t>(a.B) * a.Hkv * a.cap);
   const int box_rows = paged ? a.bs : kTK;
   CUtensorMap tmk, tmv;
-  if (!encode_rows_map(&tmk, prefix ? a.pk : a.k, store, D, 2, box_rows) ||
-      !encode_rows_map(&tmv, prefix ? a.pv : a.v, store, D, 2, box_rows))
+  if (!encode_rows_map(&tmk, prefix ? a.pk : a.k, store, D, fp8 ? 1 : 2, box_rows) ||
+      !encode_rows_map(&tmv, prefix ? a.pv : a.v, store, D, fp8 ? 1 : 2, box_rows))
     return cudaErrorInvalidValue;
   const int64_t qt = kTileRows / a.G;
   const int64_t items = prefix ? (a.T + qt - 1) / qt : (a.cu_q != nullptr ? a.T / qt + a.B : a.B);
   const dim3 grid(static_cast<unsigned>(items), static_cast<unsigned>(a.Hkv),
                   static_cast<unsigned>(prefix ? a.prefix_splits : a.own_splits));
-  return D == 128 ? launch_tile_d<128>(a, grid, prefix, tmk, tmv, box_rows, static_cast<int>(store), st)
-                  : launch_tile_d<64>(a, grid, prefix, tmk, tmv, box_rows, static_cast<int>(store), st);
+  const int rows = static_cast<int>(store);
+  if (fp8) return launch_tile_d<128, true>(a, grid, prefix, tmk, tmv, box_rows, rows, st);
+  return D == 128 ? launch_tile_d<128, false>(a, grid, prefix, tmk, tmv, box_rows, rows, st)
+                  : launch_tile_d<64, false>(a, grid, prefix, tmk, tmv, box_rows, rows, st);
 }
 
 }  // namespace eta
