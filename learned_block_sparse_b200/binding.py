@@ -7,7 +7,6 @@ library is missing, importing this module raises: there is no fallback.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -201,17 +200,14 @@ def make_shape(batch, n_q_heads, n_kv_heads, head_dim, block_size, capacity, kv_
                  _dtype_code(q_dtype) if isinstance(q_dtype, torch.dtype) else q_dtype)
 
 
-_HERE = contextlib.nullcontext()
+# The calls for new tokens are a few microseconds of GPU work in a decode step, so
+# their host side counts: raw stream handles and pointers as plain integers.
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _on(dev: torch.device):
-    """The call's device made current; nothing to do when it is."""
-    return _HERE if dev.index is None or dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
-
-
-def _token_stride(x: torch.Tensor) -> int:
-    """Elements between consecutive tokens (a single token's stride is not looked at)."""
-    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
+def _current(index: int) -> bool:
+    """Whether CUDA device `index` is the current one."""
+    return index == torch.cuda.current_device()
 
 
 def make_params(beta=5.0, z=1.0, offset_a=0.0, n_local=1, n_splits=0, gate=GATE_SIGMOID, sub_blocks=1) -> Params:
@@ -497,7 +493,10 @@ class EtaDecoder:
         self.tau = torch.empty((batch, n_q_heads), **f)
         self.out = torch.empty((batch, n_q_heads, head_dim), **f)
         self.kv_dtype, self.q_dtype = _DTYPES[self.shape.kv_dtype], _DTYPES[self.shape.q_dtype]
-        self.attend_ws = None  # see reserve_queries
+        self.attend_ws, self._reserved = None, -1  # see reserve_queries
+        self._geometry = (batch, n_q_heads, n_kv_heads, head_dim, block_size, capacity)
+        self._cache_shape = (batch, n_kv_heads, capacity, head_dim)
+        self._refs = (ctypes.byref(self.shape), ctypes.byref(self.meta_shape), ctypes.byref(self.params))
 
     @property
     def meta(self):
@@ -555,28 +554,32 @@ class EtaDecoder:
 
     # ------------------------------------------------------------- new tokens
     def _cache_args(self, k, v, block_table, num_pages, seq_lens, cu, what):
-        """Checks of the tensors the calls for new tokens share; the page arguments."""
-        s, dev = self.shape, k.device
-        if k.dtype != self.kv_dtype or v.dtype != self.kv_dtype:
+        """Checks of the tensors the calls for new tokens share: (page argument, device index)."""
+        B, _, Hkv, d, bs, cap = self._geometry
+        dev = k.get_device()
+        if dev != self.ws.get_device():
+            raise ValueError(f"{what}: K is not on this decoder's device")
+        if k.dtype is not self.kv_dtype or v.dtype is not self.kv_dtype:
             raise TypeError(f"{what}: K, V are not {self.kv_dtype}")
         if block_table is None:
-            want, pages = (s.batch, s.n_kv_heads, s.capacity, s.head_dim), None
+            want, pages = self._cache_shape, None
         else:
-            num_pages = k.shape[0] if not num_pages else num_pages
-            want = (num_pages, s.n_kv_heads, s.block_size, s.head_dim)
-            if block_table.dtype != torch.int32 or not block_table.is_contiguous() or \
-                    block_table.numel() != s.batch * (s.capacity // s.block_size) or block_table.device != dev:
+            num_pages = num_pages or k.shape[0]
+            want = (num_pages, Hkv, bs, d)
+            if block_table.dtype is not torch.int32 or block_table.numel() != B * (cap // bs) or \
+                    not block_table.is_contiguous() or block_table.get_device() != dev:
                 raise ValueError(f"{what}: block_table is int32 [B][capacity / block_size], contiguous, beside K")
             pages = ctypes.byref(Pages(block_table.data_ptr(), num_pages))
-        if k.shape != want or v.shape != want or not k.is_contiguous() or not v.is_contiguous() or v.device != dev:
+        if k.shape != want or v.shape != want or not k.is_contiguous() or not v.is_contiguous() or \
+                v.get_device() != dev:
             raise ValueError(f"{what}: K, V are contiguous tensors of shape {want} on one device")
-        if seq_lens is not None and (seq_lens.dtype != torch.int32 or seq_lens.numel() != s.batch or
-                                     not seq_lens.is_contiguous() or seq_lens.device != dev):
+        if seq_lens is not None and (seq_lens.dtype is not torch.int32 or seq_lens.numel() != B or
+                                     not seq_lens.is_contiguous() or seq_lens.get_device() != dev):
             raise ValueError(f"{what}: seq_lens is int32 [B], contiguous, beside K")
-        if cu is not None and (cu.dtype != torch.int32 or cu.numel() != s.batch + 1 or not cu.is_contiguous() or
-                               cu.device != dev):
+        if cu is not None and (cu.dtype is not torch.int32 or cu.numel() != B + 1 or not cu.is_contiguous() or
+                               cu.get_device() != dev):
             raise ValueError(f"{what}: the packed tokens' offsets are int32 [B + 1], contiguous, beside K")
-        return pages
+        return pages, dev
 
     def append(self, k_new, v_new, k, v, n_tokens: int, q: Optional[torch.Tensor] = None, rope: Optional[Rope] = None,
                seq_lens: Optional[torch.Tensor] = None, cu_new: Optional[torch.Tensor] = None,
@@ -589,78 +592,92 @@ class EtaDecoder:
         tokens may be strided (parts of a fused projection). Lengths (``n_tokens``,
         ``seq_lens``) count the new tokens. Returns the rotated queries: ``q_out``, or
         a new tensor."""
-        s, dev = self.shape, k.device
-        pages = self._cache_args(k, v, block_table, num_pages, seq_lens, cu_new, "append")
-        if block_table is not None and self.sub_blocks > 1:
+        pages, dev = self._cache_args(k, v, block_table, num_pages, seq_lens, cu_new, "append")
+        if not _current(dev):
+            with torch.cuda.device(dev):
+                return self.append(k_new, v_new, k, v, n_tokens, q, rope, seq_lens, cu_new, q_out, block_table,
+                                   num_pages, build_meta)
+        if pages is not None and self.sub_blocks > 1:
             raise EtaError(ETA_ERR_UNSUPPORTED, "eta_append_kv")
-        d, n = s.head_dim, k_new.shape[0]
-        for x, heads in ((k_new, s.n_kv_heads), (v_new, s.n_kv_heads), (q, s.n_q_heads)):
+        _, Hq, Hkv, d, _, _ = self._geometry
+        n = k_new.shape[0]
+        strides = []
+        for x, heads in ((k_new, Hkv), (v_new, Hkv), (q, Hq)):
             if x is None:
+                strides.append(0)
                 continue
-            if x.dtype != self.q_dtype or x.shape != (n, heads, d) or x.device != dev or x.stride(2) != 1 or \
-                    (heads > 1 and x.stride(1) != d):
+            at = x.stride()
+            if x.dtype is not self.q_dtype or x.shape != (n, heads, d) or x.get_device() != dev or at[2] != 1 or \
+                    (heads > 1 and at[1] != d):
                 raise ValueError(f"append: new tokens are {self.q_dtype} [n][heads][d] beside K, heads contiguous")
+            strides.append(at[0] if n > 1 else heads * d)  # (a single token's stride means nothing)
+        q_ptr = out_ptr = None
         if q is not None:
             if q_out is None:
-                q_out = torch.empty((n, s.n_q_heads, d), dtype=self.q_dtype, device=dev)
-            elif q_out.dtype != self.q_dtype or q_out.shape != q.shape or not q_out.is_contiguous() or \
-                    q_out.device != dev:
+                q_out = torch.empty((n, Hq, d), dtype=self.q_dtype, device=k.device)
+            elif q_out.dtype is not self.q_dtype or q_out.shape != q.shape or not q_out.is_contiguous() or \
+                    q_out.get_device() != dev:
                 raise ValueError("append: q_out is contiguous, of q's shape, type and device")
+            q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
         elif q_out is not None:
             raise ValueError("append: q_out without q")
-        tokens = Tokens(None if q is None else q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
-                        None if q is None else q_out.data_ptr(), 0 if q is None else _token_stride(q),
-                        _token_stride(k_new), _token_stride(v_new), None if cu_new is None else cu_new.data_ptr(), n)
+        tokens = Tokens(q_ptr, k_new.data_ptr(), v_new.data_ptr(), out_ptr, strides[2], strides[0], strides[1],
+                        None if cu_new is None else cu_new.data_ptr(), n)
         meta = Meta(self.mu.data_ptr(), self.var.data_ptr(), self.maxnorm.data_ptr()) if build_meta else Meta()
-        with _on(dev):
-            _check(lib.eta_append_kv(ctypes.byref(self.meta_shape), ctypes.byref(tokens),
-                                     ctypes.byref(_NO_ROPE if rope is None else rope.args), _ptr(k), _ptr(v), pages,
-                                     _ptr(seq_lens), n_tokens, meta, _ptr(self.ws), self.ws.numel(), _stream()),
-                   "eta_append_kv")
+        status = lib.eta_append_kv(self._refs[1], ctypes.byref(tokens),
+                                   ctypes.byref(_NO_ROPE if rope is None else rope.args), k.data_ptr(), v.data_ptr(),
+                                   pages, None if seq_lens is None else seq_lens.data_ptr(), n_tokens, meta,
+                                   self.ws.data_ptr(), self.ws.numel(), _raw_stream(dev))
+        if status != ETA_OK:
+            raise EtaError(status, "eta_append_kv")
         return q_out
 
     def reserve_queries(self, n: int) -> None:
         """Workspace of :meth:`window` and :meth:`shared` for calls of up to ``n`` new
         tokens. A larger call reserves for itself, which allocates: reserve the
         largest before capturing a CUDA graph."""
-        with _on(self.device):
-            need = lib.eta_attend_workspace_bytes(ctypes.byref(self.shape), n, 1)
+        if n <= self._reserved:
+            return
+        with torch.cuda.device(self.mu.device):
+            need = lib.eta_attend_workspace_bytes(self._refs[0], n, 1)
             if need == 0:
                 raise EtaError(ETA_ERR_INVALID_ARG, "eta_attend_workspace_bytes")
-            if self.attend_ws is not None and self.attend_ws.numel() >= need:
-                return
             if torch.cuda.is_current_stream_capturing():
                 raise RuntimeError("reserve_queries: reserve before capturing")
-            ws = torch.empty(need + 256, dtype=torch.uint8, device=self.device)
+            ws = torch.empty(need + 256, dtype=torch.uint8, device=self.mu.device)
             off = (-ws.data_ptr()) % 256
             ws = ws[off:off + need]
             _check(lib.eta_workspace_init(_ptr(ws), need, _stream()), "eta_workspace_init")
-            self.attend_ws = ws
+            self.attend_ws, self._reserved = ws, n
 
-    def _query_args(self, q, tau, tau_batch_stride, cu_q, out, what):
-        s, dev = self.shape, q.device
+    def _query_args(self, q, tau, tau_batch_stride, cu_q, out, dev, what):
+        _, Hq, _, d, _, _ = self._geometry
         n = q.shape[0]
-        if q.dtype != self.q_dtype or q.shape != (n, s.n_q_heads, s.head_dim) or not q.is_contiguous():
-            raise ValueError(f"{what}: q is contiguous {self.q_dtype} [n][Hq][d]")
+        if q.dtype is not self.q_dtype or q.shape != (n, Hq, d) or not q.is_contiguous() or q.get_device() != dev:
+            raise ValueError(f"{what}: q is contiguous {self.q_dtype} [n][Hq][d] beside K")
         if out is None:
             if cu_q is not None:
                 raise ValueError(f"{what}: packed queries need out")
             out = self.out
-        if out.dtype not in (torch.float32, torch.bfloat16) or out.shape != q.shape or not out.is_contiguous() or \
-                out.device != dev:
-            raise ValueError(f"{what}: out is contiguous fp32 or bf16, of q's shape and device")
+        if out.dtype is torch.float32:
+            code = ETA_F32
+        elif out.dtype is torch.bfloat16:
+            code = ETA_BF16
+        else:
+            raise TypeError(f"{what}: out is fp32 or bf16")
+        if out.shape != q.shape or not out.is_contiguous() or out.get_device() != dev:
+            raise ValueError(f"{what}: out is contiguous, of q's shape, beside K")
+        tau_ptr, stride = None, 0
         if tau is not None:
-            if tau.dtype != torch.float32 or not tau.is_contiguous() or tau.device != dev or \
-                    tau.shape not in ((s.n_q_heads,), (n, s.n_q_heads)):
-                raise ValueError(f"{what}: tau is contiguous fp32 [Hq] or [n][Hq] beside q")
-            if tau_batch_stride is None:
-                tau_batch_stride = 0 if tau.dim() == 1 else s.n_q_heads
-            elif tau_batch_stride not in (0, s.n_q_heads) or (tau_batch_stride and tau.dim() == 1):
+            if tau.dtype is not torch.float32 or not tau.is_contiguous() or tau.get_device() != dev or \
+                    tau.shape not in ((Hq,), (n, Hq)):
+                raise ValueError(f"{what}: tau is contiguous fp32 [Hq] or [n][Hq] beside K")
+            stride = (0 if tau.dim() == 1 else Hq) if tau_batch_stride is None else tau_batch_stride
+            if stride not in (0, Hq) or (stride and tau.dim() == 1):
                 raise ValueError(f"{what}: tau_batch_stride is 0 or Hq, within tau")
-        queries = Queries(q.data_ptr(), None if cu_q is None else cu_q.data_ptr(), n,
-                          None if tau is None else tau.data_ptr(), tau_batch_stride or 0, out.data_ptr(),
-                          ETA_F32 if out.dtype == torch.float32 else ETA_BF16)
-        return queries, out
+            tau_ptr = tau.data_ptr()
+        return ctypes.byref(Queries(q.data_ptr(), None if cu_q is None else cu_q.data_ptr(), n, tau_ptr, stride,
+                                    out.data_ptr(), code)), out
 
     def window(self, q, k, v, n_tokens: int, window: int, sinks: int = 0, seq_lens: Optional[torch.Tensor] = None,
                cu_q: Optional[torch.Tensor] = None, tau: Optional[torch.Tensor] = None,
@@ -669,17 +686,20 @@ class EtaDecoder:
         """Attention of new tokens over the last ``window`` tokens (their own among
         them) and the first ``sinks`` tokens of their row. ``q`` [n][Hq][d]: one token
         per row, or packed tokens with ``cu_q`` (int32 [B + 1]; needs ``out``). With
-        ``tau`` ([Hq] or [n][Hq]) logits are gated as in :meth:`dense`."""
-        pages = self._cache_args(k, v, block_table, num_pages, seq_lens, cu_q, "window")
-        queries, out = self._query_args(q, tau, tau_batch_stride, cu_q, out, "window")
-        if q.device != k.device:
-            raise ValueError("window: q and K are on different devices")
+        ``tau`` ([Hq] or [n][Hq]) logits are gated as in :meth:`dense`. ``out`` is fp32
+        or bf16."""
+        pages, dev = self._cache_args(k, v, block_table, num_pages, seq_lens, cu_q, "window")
+        if not _current(dev):
+            with torch.cuda.device(dev):
+                return self.window(q, k, v, n_tokens, window, sinks, seq_lens, cu_q, tau, tau_batch_stride, out,
+                                   block_table, num_pages)
+        queries, out = self._query_args(q, tau, tau_batch_stride, cu_q, out, dev, "window")
         self.reserve_queries(q.shape[0])
-        with _on(q.device):
-            _check(lib.eta_attend_window(ctypes.byref(self.shape), ctypes.byref(self.params), ctypes.byref(queries),
-                                         _ptr(k), _ptr(v), pages, _ptr(seq_lens), n_tokens, window, sinks,
-                                         _ptr(self.attend_ws), self.attend_ws.numel(), _stream()),
-                   "eta_attend_window")
+        status = lib.eta_attend_window(self._refs[0], self._refs[2], queries, k.data_ptr(), v.data_ptr(), pages,
+                                       None if seq_lens is None else seq_lens.data_ptr(), n_tokens, window, sinks,
+                                       self.attend_ws.data_ptr(), self.attend_ws.numel(), _raw_stream(dev))
+        if status != ETA_OK:
+            raise EtaError(status, "eta_attend_window")
         return out
 
     def shared(self, q, k, v, n_tokens: int, prefix: Prefix, seq_lens: Optional[torch.Tensor] = None,
@@ -689,26 +709,28 @@ class EtaDecoder:
         """Attention of new tokens over a :class:`Prefix` that all rows share, read
         once, and over their own cached tokens (``n_tokens``, ``seq_lens`` count the
         row's own). Other arguments as :meth:`window`."""
-        pages = self._cache_args(k, v, block_table, num_pages, seq_lens, cu_q, "shared")
-        queries, out = self._query_args(q, tau, tau_batch_stride, cu_q, out, "shared")
-        s = self.shape
-        if q.device != k.device:
-            raise ValueError("shared: q and K are on different devices")
+        pages, dev = self._cache_args(k, v, block_table, num_pages, seq_lens, cu_q, "shared")
+        if not _current(dev):
+            with torch.cuda.device(dev):
+                return self.shared(q, k, v, n_tokens, prefix, seq_lens, cu_q, tau, tau_batch_stride, out, block_table,
+                                   num_pages)
+        queries, out = self._query_args(q, tau, tau_batch_stride, cu_q, out, dev, "shared")
+        _, _, Hkv, d, bs, _ = self._geometry
         if prefix.n_tokens > 0:
-            if (prefix.blocks is None) != (block_table is None):
+            if (prefix.blocks is None) != (pages is None):
                 raise ValueError("shared: the prefix lies in the pools exactly when the rows do")
-            if prefix.k is not None and (prefix.k.dtype != self.kv_dtype or prefix.k.device != q.device or
-                                         (prefix.k.shape[0], prefix.k.shape[2]) != (s.n_kv_heads, s.head_dim)):
-                raise ValueError(f"shared: prefix k, v are {self.kv_dtype} [Hkv][capacity][d] beside q")
-            if prefix.blocks is not None and (prefix.blocks.device != q.device or
-                                              prefix.blocks.numel() < -(-prefix.n_tokens // s.block_size)):
-                raise ValueError("shared: prefix blocks cover n_tokens, beside q")
+            if prefix.k is not None and (prefix.k.dtype is not self.kv_dtype or prefix.k.get_device() != dev or
+                                         (prefix.k.shape[0], prefix.k.shape[2]) != (Hkv, d)):
+                raise ValueError(f"shared: prefix k, v are {self.kv_dtype} [Hkv][capacity][d] beside K")
+            if prefix.blocks is not None and (prefix.blocks.get_device() != dev or
+                                              prefix.blocks.numel() < -(-prefix.n_tokens // bs)):
+                raise ValueError("shared: prefix blocks cover n_tokens, beside K")
         self.reserve_queries(q.shape[0])
-        with _on(q.device):
-            _check(lib.eta_attend_shared(ctypes.byref(s), ctypes.byref(self.params), ctypes.byref(queries),
-                                         ctypes.byref(prefix.args), _ptr(k), _ptr(v), pages, _ptr(seq_lens), n_tokens,
-                                         _ptr(self.attend_ws), self.attend_ws.numel(), _stream()),
-                   "eta_attend_shared")
+        status = lib.eta_attend_shared(self._refs[0], self._refs[2], queries, ctypes.byref(prefix.args), k.data_ptr(),
+                                       v.data_ptr(), pages, None if seq_lens is None else seq_lens.data_ptr(),
+                                       n_tokens, self.attend_ws.data_ptr(), self.attend_ws.numel(), _raw_stream(dev))
+        if status != ETA_OK:
+            raise EtaError(status, "eta_attend_shared")
         return out
 
     def device_status(self) -> int:

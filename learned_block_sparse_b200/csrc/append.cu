@@ -18,7 +18,10 @@
 // full it can build the metadata behind a __syncthreads(), with no second launch
 // and no inter-block ordering. One warp takes one token; a lane owns two 2-element
 // words of every row of the token (the two halves of its pairs), so its two angles
-// are evaluated once and serve all HB * (G + 1) rows.
+// are evaluated once and serve all HB * (G + 1) rows, whose loads are in flight
+// meanwhile.
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 #include "launch.h"
 
@@ -125,14 +128,32 @@ __device__ __forceinline__ float key_value(double x) { return to_odd(x); }
 template <>
 __device__ __forceinline__ float key_value<float>(double x) { return __double2float_rn(x); }
 
+// The coordinates of one 32-bit word of the cache, widened exactly (e4m3 through f16).
 template <typename KV>
-__device__ __forceinline__ float cache_elem(uint32_t w, int p);
+__device__ __forceinline__ void cache_word(uint32_t w, float (&x)[4 / KvTraits<KV>::kBytes]);
 template <>
-__device__ __forceinline__ float cache_elem<float>(uint32_t w, int) { return __uint_as_float(w); }
+__device__ __forceinline__ void cache_word<float>(uint32_t w, float (&x)[1]) {
+  x[0] = __uint_as_float(w);
+}
 template <>
-__device__ __forceinline__ float cache_elem<Bf16Raw>(uint32_t w, int p) { return p == 0 ? bf16_lo(w) : bf16_hi(w); }
+__device__ __forceinline__ void cache_word<Bf16Raw>(uint32_t w, float (&x)[2]) {
+  x[0] = bf16_lo(w);
+  x[1] = bf16_hi(w);
+}
 template <>
-__device__ __forceinline__ float cache_elem<Fp8Raw>(uint32_t w, int p) { return e4m3_to_float((w >> (8 * p)) & 0xffu); }
+__device__ __forceinline__ void cache_word<Fp8Raw>(uint32_t w, float (&x)[4]) {
+  uint32_t lo, hi;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  x[0] = a.x;
+  x[1] = a.y;
+  x[2] = b.x;
+  x[3] = b.y;
+}
 
 // The metadata of a full block, split over the warps of a thread block: part 0
 // the row norms (lane = row), parts 1..WL the column sums of 32 words each
@@ -156,12 +177,12 @@ __device__ __forceinline__ void meta_part(const unsigned char* base, int bs, int
         const uint4 u = row[c];
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i) {
+          float x[P];
+          cache_word<KV>(w[i], x);
 #pragma unroll
-          for (int p = 0; p < P; ++p) {
-            const float x = cache_elem<KV>(w[i], p);
-            nr = __fmaf_rn(x, x, nr);
-          }
+          for (int p = 0; p < P; ++p) nr = __fmaf_rn(x[p], x[p], nr);
+        }
       }
       best = fmaxf(best, nr);
     }
@@ -176,18 +197,20 @@ __device__ __forceinline__ void meta_part(const unsigned char* base, int bs, int
   for (int p = 0; p < P; ++p) t[p] = v[p] = 0.0f;
 #pragma unroll 16
   for (int r = 0; r < bs; ++r) {
-    const uint32_t w = words[static_cast<int64_t>(r) * WPR];
+    float x[P];
+    cache_word<KV>(words[static_cast<int64_t>(r) * WPR], x);
 #pragma unroll
-    for (int p = 0; p < P; ++p) t[p] = __fadd_rn(t[p], cache_elem<KV>(w, p));
+    for (int p = 0; p < P; ++p) t[p] = __fadd_rn(t[p], x[p]);
   }
 #pragma unroll
   for (int p = 0; p < P; ++p) t[p] = __fdiv_rn(t[p], rows);
 #pragma unroll 16
   for (int r = 0; r < bs; ++r) {
-    const uint32_t w = words[static_cast<int64_t>(r) * WPR];
+    float x[P];
+    cache_word<KV>(words[static_cast<int64_t>(r) * WPR], x);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      const float e = __fsub_rn(cache_elem<KV>(w, p), t[p]);
+      const float e = __fsub_rn(x[p], t[p]);
       v[p] = __fmaf_rn(e, e, v[p]);
     }
   }
@@ -199,11 +222,13 @@ __device__ __forceinline__ void meta_part(const unsigned char* base, int bs, int
   }
 }
 
-template <typename QT, typename KV, int D>
+// SINGLE: one new token per row of the batch, whose rows (key, value, queries) the
+// warps share; else a warp (at d = 64 each half of one) takes whole tokens.
+template <typename QT, typename KV, int D, int G, bool SINGLE>
 __global__ void __launch_bounds__(kAppWarps * 32) append_kernel(const AppendArgs a) {
   constexpr int EB = KvTraits<KV>::kBytes;
   constexpr int LPR = D / 4;        // lanes per row: each owns two words
-  constexpr int RPW = 32 / LPR;     // rows a warp works on at once
+  constexpr int TPW = 32 / LPR;     // tokens a warp works on at once
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int item = blockIdx.x, bs = a.bs, sh = a.bs_log2;
   grid_dependency_wait();
@@ -214,7 +239,7 @@ __global__ void __launch_bounds__(kAppWarps * 32) append_kernel(const AppendArgs
   // floor(n_b / bs) + 2 blocks <= s_{b+1} - s_b, so no prefix sum is needed.
   int b = item;
   int64_t t0 = item, fresh = 1, j = 0;
-  if (a.cu_new != nullptr) {
+  if (!SINGLE) {
     if (threadIdx.x == 0 && blockIdx.y == 0 && item < a.B) {  // every row's bounds are looked at once
       const int64_t c0 = a.cu_new[item], c1 = a.cu_new[item + 1];
       if (c0 < 0 || c1 < c0 || c1 > a.T) atomicExch(a.status, static_cast<int32_t>(ETA_ERR_INVALID_ARG));
@@ -233,7 +258,7 @@ __global__ void __launch_bounds__(kAppWarps * 32) append_kernel(const AppendArgs
     if (j < 0) return;
   }
   const int64_t len = a.seq_lens != nullptr ? static_cast<int64_t>(__ldg(a.seq_lens + b)) : a.n;
-  if (len == 0 && a.cu_new == nullptr) return;  // an idle row of a padded batch
+  if (SINGLE && len == 0) return;  // an idle row of a padded batch
   if (len < fresh || len > a.n) {
     if (threadIdx.x == 0) atomicExch(a.status, static_cast<int32_t>(ETA_ERR_INVALID_ARG));
     return;
@@ -244,7 +269,7 @@ __global__ void __launch_bounds__(kAppWarps * 32) append_kernel(const AppendArgs
   if (slot0 >= slot1) return;
 
   const int kv0 = blockIdx.y * a.HB;
-  const int nkv = min(a.HB, a.Hkv - kv0), G = a.Hq / a.Hkv;
+  const int nkv = min(a.HB, a.Hkv - kv0);
   // store row of the block's token 0 for kv head kv0, and the rows between heads
   int64_t row0, head_rows;
   bool page_ok = true;
@@ -271,64 +296,68 @@ __global__ void __launch_bounds__(kAppWarps * 32) append_kernel(const AppendArgs
     f0 = __ldg(a.inv_freq + (a.pairs_adjacent ? w : 2 * w));
     f1 = __ldg(a.inv_freq + (a.pairs_adjacent ? w + quarter : 2 * w + 1));
   }
-  const int rows = nkv * (G + 2);  // per kv head: the key, the value, G queries
+  const int off = static_cast<int>(slot0 - (blk << sh));  // first new row of the block
+  const int count = static_cast<int>(slot1 - slot0);
+  const bool have_q = a.q != nullptr;
 
-  for (int64_t slot = slot0 + warp; slot < slot1; slot += kAppWarps) {
-    const int64_t tok = t0 + (slot - first);
+  for (int i = SINGLE ? sub : warp * TPW + sub; i < count; i += kAppWarps * TPW) {
+    const int64_t tok = t0 + (slot0 - first) + i;
+    const int64_t k_at = tok * a.k_stride + static_cast<int64_t>(kv0) * D;
+    const int64_t v_at = tok * a.v_stride + static_cast<int64_t>(kv0) * D;
+    const int64_t q_at = tok * a.q_stride + static_cast<int64_t>(kv0) * G * D;
+    const int64_t o_at = (tok * a.Hq + static_cast<int64_t>(kv0) * G) * D;
+    const int64_t c_at = (row0 + off + i) * D;
     double s0 = 0.0, c0 = 1.0, s1 = 0.0, c1 = 1.0;
-    if (turns) {
-      sincos_reduced(static_cast<double>(slot) * f0, s0, c0);
-      sincos_reduced(static_cast<double>(slot) * f1, s1, c1);
-    }
-    const float s0f = static_cast<float>(s0), c0f = static_cast<float>(c0);
-    const float s1f = static_cast<float>(s1), c1f = static_cast<float>(c1);
-    constexpr int U = 4;  // rows in flight per lane
-    for (int r0 = 0; r0 < rows; r0 += U * RPW) {
-      float2 x[U], y[U];
+    float s0f = 0.0f, c0f = 1.0f, s1f = 0.0f, c1f = 1.0f;
+    bool angles = false;
+    for (int h = 0; h < nkv; ++h) {
+      // all rows of the head are in flight (the first time, during the angles)
+      float2 x[G + 2], y[G + 2];  // the key, the value, G queries
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int r = r0 + u * RPW + sub;
-        x[u] = y[u] = make_float2(0.0f, 0.0f);
-        if (r >= rows) continue;
-        const int h = r / (G + 2), g = r - h * (G + 2);
-        const void* src = g == 0 ? a.k : (g == 1 ? a.v : a.q);
-        if (src == nullptr) continue;
-        const int64_t at = g == 0 ? tok * a.k_stride + static_cast<int64_t>(kv0 + h) * D
-                                  : (g == 1 ? tok * a.v_stride + static_cast<int64_t>(kv0 + h) * D
-                                            : tok * a.q_stride + static_cast<int64_t>((kv0 + h) * G + g - 2) * D);
-        x[u] = load_word<QT>(src, at + e0);
-        y[u] = load_word<QT>(src, at + e1);
+      for (int r = 0; r < G + 2; ++r) {
+        if (SINGLE && (r & (kAppWarps - 1)) != warp) continue;
+        if (r >= 2 && !have_q) continue;
+        const void* src = r == 0 ? a.k : (r == 1 ? a.v : a.q);
+        const int64_t at = r == 0 ? k_at + h * D : (r == 1 ? v_at + h * D : q_at + (h * G + r - 2) * D);
+        x[r] = load_word<QT>(src, at + e0);
+        y[r] = load_word<QT>(src, at + e1);
+      }
+      if (!angles && turns) {
+        const double pos = static_cast<double>(slot0 + i);
+        sincos_reduced(pos * f0, s0, c0);
+        sincos_reduced(pos * f1, s1, c1);
+        s0f = static_cast<float>(s0), c0f = static_cast<float>(c0);
+        s1f = static_cast<float>(s1), c1f = static_cast<float>(c1);
+        angles = true;
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int r = r0 + u * RPW + sub;
-        if (r >= rows) continue;
-        const int h = r / (G + 2), g = r - h * (G + 2);
-        if (g <= 1) {
+      for (int r = 0; r < G + 2; ++r) {
+        if (SINGLE && (r & (kAppWarps - 1)) != warp) continue;
+        if (r <= 1) {
           if (!page_ok) continue;
-          const int64_t at = (row0 + static_cast<int64_t>(h) * head_rows + (slot - (blk << sh))) * D;
-          if (g == 1 || !turns) {
-            void* dst = g == 1 ? a.vc : a.kc;
-            store_word<KV>(dst, at + e0, x[u].x, x[u].y);
-            store_word<KV>(dst, at + e1, y[u].x, y[u].y);
+          const int64_t at = c_at + h * head_rows * D;
+          if (r == 1 || !turns) {
+            void* dst = r == 1 ? a.vc : a.kc;
+            store_word<KV>(dst, at + e0, x[r].x, x[r].y);
+            store_word<KV>(dst, at + e1, y[r].x, y[r].y);
           } else if (a.pairs_adjacent) {
-            const double p = x[u].x, q = x[u].y, m = y[u].x, n = y[u].y;
+            const double p = x[r].x, q = x[r].y, m = y[r].x, n = y[r].y;
             store_word<KV>(a.kc, at + e0, key_value<KV>(fma(p, c0, -(q * s0))), key_value<KV>(fma(q, c0, p * s0)));
             store_word<KV>(a.kc, at + e1, key_value<KV>(fma(m, c1, -(n * s1))), key_value<KV>(fma(n, c1, m * s1)));
           } else {
-            const double p = x[u].x, q = x[u].y, m = y[u].x, n = y[u].y;
+            const double p = x[r].x, q = x[r].y, m = y[r].x, n = y[r].y;
             store_word<KV>(a.kc, at + e0, key_value<KV>(fma(p, c0, -(m * s0))), key_value<KV>(fma(q, c1, -(n * s1))));
             store_word<KV>(a.kc, at + e1, key_value<KV>(fma(m, c0, p * s0)), key_value<KV>(fma(n, c1, q * s1)));
           }
-        } else if (a.q != nullptr) {
-          const int64_t at = (tok * a.Hq + (kv0 + h) * G + g - 2) * D;
-          float2 p = x[u], q = y[u];
+        } else if (have_q) {
+          const int64_t at = o_at + (h * G + r - 2) * D;
+          float2 p = x[r], q = y[r];
           if (turns && a.pairs_adjacent) {
-            p = make_float2(x[u].x * c0f - x[u].y * s0f, x[u].y * c0f + x[u].x * s0f);
-            q = make_float2(y[u].x * c1f - y[u].y * s1f, y[u].y * c1f + y[u].x * s1f);
+            p = make_float2(x[r].x * c0f - x[r].y * s0f, x[r].y * c0f + x[r].x * s0f);
+            q = make_float2(y[r].x * c1f - y[r].y * s1f, y[r].y * c1f + y[r].x * s1f);
           } else if (turns) {
-            p = make_float2(x[u].x * c0f - y[u].x * s0f, x[u].y * c1f - y[u].y * s1f);
-            q = make_float2(y[u].x * c0f + x[u].x * s0f, y[u].y * c1f + x[u].y * s1f);
+            p = make_float2(x[r].x * c0f - y[r].x * s0f, x[r].y * c1f - y[r].y * s1f);
+            q = make_float2(y[r].x * c0f + x[r].x * s0f, y[r].y * c1f + x[r].y * s1f);
           }
           store_word<QT>(a.q_out, at + e0, p.x, p.y);
           store_word<QT>(a.q_out, at + e1, q.x, q.y);
@@ -350,24 +379,37 @@ __global__ void __launch_bounds__(kAppWarps * 32) append_kernel(const AppendArgs
   }
 }
 
-template <typename QT, typename KV>
-cudaError_t launch_append_t(const AppendArgs& a, int D, int64_t items, cudaStream_t st) {
-  dim3 grid(static_cast<unsigned>(items), static_cast<unsigned>((a.Hkv + a.HB - 1) / a.HB));
+template <typename QT, typename KV, int D, int G>
+cudaError_t launch_append_g(const AppendArgs& a, int64_t items, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
+  cfg.gridDim = dim3(static_cast<unsigned>(items), static_cast<unsigned>((a.Hkv + a.HB - 1) / a.HB));
   cfg.blockDim = dim3(kAppWarps * 32);
   cfg.stream = st;
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e;
-  if constexpr (KvTraits<KV>::kBytes == 1) {
-    e = cudaLaunchKernelEx(&cfg, append_kernel<QT, KV, 128>, a);
-  } else {
-    e = D == 128 ? cudaLaunchKernelEx(&cfg, append_kernel<QT, KV, 128>, a)
-                 : cudaLaunchKernelEx(&cfg, append_kernel<QT, KV, 64>, a);
-  }
+  const cudaError_t e = a.cu_new == nullptr ? cudaLaunchKernelEx(&cfg, append_kernel<QT, KV, D, G, true>, a)
+                                            : cudaLaunchKernelEx(&cfg, append_kernel<QT, KV, D, G, false>, a);
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <typename QT, typename KV, int D>
+cudaError_t launch_append_d(const AppendArgs& a, int64_t items, cudaStream_t st) {
+  switch (a.Hq / a.Hkv) {
+    case 1: return launch_append_g<QT, KV, D, 1>(a, items, st);
+    case 2: return launch_append_g<QT, KV, D, 2>(a, items, st);
+    case 4: return launch_append_g<QT, KV, D, 4>(a, items, st);
+    default: return launch_append_g<QT, KV, D, 8>(a, items, st);
+  }
+}
+
+template <typename QT, typename KV>
+cudaError_t launch_append_t(const AppendArgs& a, int D, int64_t items, cudaStream_t st) {
+  if constexpr (KvTraits<KV>::kBytes == 1) {
+    return launch_append_d<QT, KV, 128>(a, items, st);
+  } else {
+    return D == 128 ? launch_append_d<QT, KV, 128>(a, items, st) : launch_append_d<QT, KV, 64>(a, items, st);
+  }
 }
 
 }  // namespace
@@ -406,7 +448,11 @@ cudaError_t launch_append(const AppendCall& c, cudaStream_t st) {
   a.bs_log2 = 0;
   while ((1 << a.bs_log2) < s.block_size) ++a.bs_log2;
   const int64_t items = a.cu_new == nullptr ? s.batch : a.T / a.bs + 2 * static_cast<int64_t>(s.batch);
+  // kv heads per thread block: more share a token's angles, as long as four thread
+  // blocks per SM remain
   a.HB = 1;
+  while (a.cu_new != nullptr && 2 * a.HB <= a.Hkv && items * a.Hkv >= 8 * static_cast<int64_t>(a.HB) * device_sm_count())
+    a.HB *= 2;
   const bool qf32 = s.q_dtype == ETA_F32;
   switch (s.kv_dtype) {
     case ETA_FP8_E4M3: return launch_append_t<Bf16Raw, Fp8Raw>(a, s.head_dim, items, st);
