@@ -9,9 +9,10 @@
 // One thread block takes one (row, kv head) and a range of its key chunks; its four
 // warps take chunks in turn. Every warp streams for itself: lane 0 arms a barrier and
 // starts the tensor copies of a chunk (8 KB of K and V: 16 keys of bf16 at d = 128,
-// 32 of fp8 or at d = 64) into one of the warp's three buffers, two chunks ahead of the one
-// being attended, so warps never wait for one another before the final merge. Two
-// thread blocks fit per SM (96 KB each): 128 KB in flight.
+// 32 of fp8 or at d = 64) into one of the warp's two buffers while the other is
+// attended, so warps never wait for one another before the final merge. Three
+// thread blocks fit per SM (64 KB each): 96 KB in flight, and three warps per
+// scheduler hide each other's dependent chains.
 //
 // Rounding: the weights' fp32 value is split into two bf16 (f16 with fp8 values)
 // numbers, the first in rows 0-7 of the A operand, the remainder in rows 8-15, so one
@@ -30,7 +31,7 @@ namespace eta {
 
 namespace {
 
-constexpr int kRowWarps = 4, kRowBufs = 3;
+constexpr int kRowWarps = 4, kRowBufs = 2, kRowBlocks = 3;  // blocks per SM
 
 __device__ __forceinline__ void ldm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -113,13 +114,12 @@ struct RowChunk {
 };
 
 template <int D, int G, bool FP8>
-__global__ void __launch_bounds__(kRowWarps * 32, 2)
+__global__ void __launch_bounds__(kRowWarps * 32, kRowBlocks)
     attend_row_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap tmk,
                       const __grid_constant__ CUtensorMap tmv, const int box_rows, const int store_rows) {
   using C = RowChunk<D, FP8>;
   constexpr int CH = C::kKeys, NT = CH / 8, KST = D / 16, NDT = D / 8;
   extern __shared__ __align__(1024) unsigned char row_smem[];
-  unsigned char* tiles = row_smem;  // [warp][buffer][K, V]
   uint64_t* s_bar = reinterpret_cast<uint64_t*>(row_smem + kRowWarps * kRowBufs * 2 * C::kTile);
   int* s_abort = reinterpret_cast<int*>(s_bar + kRowWarps * kRowBufs);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -133,77 +133,76 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2)
   allow_dependent_launch();
   OwnTile t;
   if (!own_tile(a, blockIdx.x, 0, tid == 0 && h == 0 && split == 0, t)) return;
+  // positions, chunks and store rows of a call fit in 32 bits (the host checks the rows)
   const Visible vis = visible_of(a, t.p0, t.p0);
+  const int p0 = static_cast<int>(t.p0), a1 = static_cast<int>(vis.a1), b0 = static_cast<int>(vis.b0);
   const bool paged = a.block_table != nullptr;
-  const int64_t base_b = paged ? vis.b0 & ~static_cast<int64_t>(max(CH, box_rows) - 1) : vis.b0;
-  const int chunks_a = static_cast<int>((vis.a1 + CH - 1) / CH);
-  const int64_t chunks = chunks_a + (vis.b1 - base_b + CH - 1) / CH;
-  const int64_t c0 = chunks * split / splits, c1 = chunks * (split + 1) / splits;
-  const int n = static_cast<int>((c1 - c0 - warp + kRowWarps - 1) / kRowWarps);  // chunks of this warp (may be <= 0)
+  const int base_b = paged ? b0 & ~(CH - 1) : b0;
+  const int chunks_a = (a1 + CH - 1) / CH;
+  const int chunks = chunks_a + (p0 + CH - base_b) / CH;
+  const int c0 = static_cast<int>(static_cast<int64_t>(chunks) * split / splits);
+  const int c1 = static_cast<int>(static_cast<int64_t>(chunks) * (split + 1) / splits);
+  const int n = (c1 - c0 - warp + kRowWarps - 1) / kRowWarps;  // chunks of this warp (0 at least)
 
-  // this warp's j-th chunk: first key, and the keys [v0, v1) of it that are visible
-  auto bounds = [&](int j, int64_t& s0, int& v0, int& v1) {
-    const int64_t u = c0 + warp + static_cast<int64_t>(j) * kRowWarps;
-    int64_t lo, hi;
-    if (u < chunks_a) {
-      s0 = u * CH;
-      lo = 0;
-      hi = vis.a1;
-    } else {
-      s0 = base_b + (u - chunks_a) * CH;
-      lo = vis.b0;
-      hi = vis.b1;
-    }
-    v0 = static_cast<int>(max(int64_t{0}, min(int64_t{CH}, lo - s0)));
-    v1 = static_cast<int>(min(int64_t{CH}, hi - s0));
+  // this warp's j-th chunk: its first key, and the keys [v0, v1) of it that are visible
+  auto bounds = [&](int j, int& s0, int& v0, int& v1) {
+    const int u = c0 + warp + j * kRowWarps;
+    const bool in_a = u < chunks_a;
+    s0 = in_a ? u * CH : base_b + (u - chunks_a) * CH;
+    v0 = in_a ? 0 : max(0, b0 - s0);
+    v1 = min(CH, (in_a ? a1 : p0 + 1) - s0);
   };
-  unsigned char* mine = tiles + warp * kRowBufs * 2 * C::kTile;
+  unsigned char* mine = row_smem + warp * kRowBufs * 2 * C::kTile;  // [buffer][K, V]
   uint64_t* bar = s_bar + warp * kRowBufs;
-  // The row of lane i's box of the j-th chunk (store_rows, past the store, for a box
-  // without a visible key or page: it arrives as zeros). Whole warp.
+  const int32_t* table = paged ? a.block_table + static_cast<int64_t>(t.b) * a.nb_cap : nullptr;
+  const int seg_row = static_cast<int>((static_cast<int64_t>(t.b) * a.Hkv + h) * a.cap);
+  const bool box_lane = lane * box_rows < CH;
+  // The store row of lane i's box of the j-th chunk; store_rows, past the store, for a
+  // box without a visible key or page: it arrives as zeros.
   auto locate = [&](int j) -> int {
-    int y = store_rows;
-    if (j < n) {
-      int64_t s0;
-      int v0, v1;
-      bounds(j, s0, v0, v1);
-      const int k0 = lane * box_rows;
-      if (k0 < v1 && k0 + box_rows > v0) {
-        const int64_t r = own_row(a, t.b, h, s0 + k0);
-        if (r >= 0) y = static_cast<int>(r);
-        else atomicExch(a.status, static_cast<int32_t>(ETA_ERR_INVALID_ARG));
-      }
+    if (j >= n || !box_lane) return store_rows;
+    int s0, v0, v1;
+    bounds(j, s0, v0, v1);
+    const int k0 = lane * box_rows, s = s0 + k0;
+    if (k0 >= v1 || k0 + box_rows <= v0) return store_rows;
+    if (!paged) return seg_row + s;
+    const int page = __ldg(table + (s >> a.bs_log2));
+    if (page < 0 || page >= a.num_pages) {
+      atomicExch(a.status, static_cast<int32_t>(ETA_ERR_INVALID_ARG));
+      return store_rows;
     }
-    return y;
+    return (page * a.Hkv + h) * a.bs + (s & (a.bs - 1));
   };
-  auto issue = [&](int j, int y) {
+  auto issue = [&](int j, int buf, int y) {
     if (j >= n) return;
-    uint64_t* b = &bar[j % kRowBufs];
-    if (lane == 0) mbar_arrive_expect_tx(b, 2 * C::kTile);
+    if (lane == 0) mbar_arrive_expect_tx(&bar[buf], 2 * C::kTile);
     __syncwarp();
-    if (lane * box_rows < CH) {
-      unsigned char* kt = mine + (j % kRowBufs) * 2 * C::kTile + lane * box_rows * 128;
+    if (box_lane) {
+      unsigned char* kt = mine + buf * 2 * C::kTile + lane * box_rows * 128;
 #pragma unroll
       for (int x = 0; x < C::kBoxes; ++x) {
-        tma_load_rows(kt + x * CH * 128, &tmk, x * (128 / C::EB), y, b);
-        tma_load_rows(kt + C::kTile + x * CH * 128, &tmv, x * (128 / C::EB), y, b);
+        tma_load_rows(kt + x * CH * 128, &tmk, x * (128 / C::EB), y, &bar[buf]);
+        tma_load_rows(kt + C::kTile + x * CH * 128, &tmv, x * (128 / C::EB), y, &bar[buf]);
       }
     }
   };
-  // page state of a chunk's boxes as a mask of 16-key groups
+  // the 16-key groups of a chunk that have a page, as a mask
   auto groups_of = [&](int y) -> uint32_t {
-    uint32_t g = 0;
-    if (lane * box_rows < CH && y != store_rows) g = ((1u << (box_rows >> 4)) - 1u) << (lane * (box_rows >> 4));
-    return __reduce_or_sync(kFull, g);
+    if (!paged) return 3u;
+    const uint32_t g = ((1u << (box_rows >> 4)) - 1u) << (lane * (box_rows >> 4) & 31);
+    return __reduce_or_sync(kFull, box_lane && y != store_rows ? g : 0u);
   };
   __syncthreads();  // barriers are initialised
+  // chunks 0 .. kRowBufs - 2 start at once; y_next: the rows of the one after them,
+  // looked up a round before they are needed
   uint32_t groups = 0;  // of the chunk in each buffer, a byte each
 #pragma unroll
   for (int j = 0; j < kRowBufs - 1; ++j) {
     const int y = locate(j);
     groups |= groups_of(y) << (8 * j);
-    issue(j, y);
+    issue(j, j, y);
   }
+  int y_next = locate(kRowBufs - 1);
 
   // query fragments: row = lane / 4 (head of the group), q = lane % 4
   const int row = lane >> 2, qd = lane & 3;
@@ -266,32 +265,37 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2)
   for (int j = 0; j < NDT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
   float m = -INFINITY, l = 0.0f;  // log2 units; l: this thread's keys
   bool ok = true;
-  int issued = min(max(n, 0), kRowBufs - 1);
+  int issued = min(n, kRowBufs - 1);
 
+  // shared-memory offsets of this lane in a tile: its key row's piece (K, ldmatrix),
+  // its value row's piece (V, transposed); the swizzle makes further pieces an XOR
+  const uint32_t k_lane = static_cast<uint32_t>((lane & 7) * 128 + (((lane >> 3) ^ (lane & 7)) << 4));
+  const uint32_t v_lane = static_cast<uint32_t>((8 * ((lane >> 3) & 1) + (lane & 7)) * 128 +
+                                                (((lane >> 4) ^ (lane & 7)) << 4));
+  const uint32_t tiles0 = smem_u32(mine);
+  int buf = 0, round = 0;
   for (int j = 0; j < n; ++j) {
-    const int buf = j % kRowBufs;
     // the next copies first: their buffer was released at the end of the last round
     {
-      const int y = locate(j + kRowBufs - 1), at = 8 * ((j + kRowBufs - 1) % kRowBufs);
-      groups = (groups & ~(0xffu << at)) | (groups_of(y) << at);
-      issue(j + kRowBufs - 1, y);
+      const int into = buf == 0 ? kRowBufs - 1 : buf - 1;
+      groups = (groups & ~(0xffu << (8 * into))) | (groups_of(y_next) << (8 * into));
+      issue(j + kRowBufs - 1, into, y_next);
       if (j + kRowBufs - 1 < n) issued = j + kRowBufs;
+      y_next = locate(j + kRowBufs);
     }
-    ok = mbar_wait_bounded(&bar[buf], (j / kRowBufs) & 1, s_abort, a.status);
+    ok = mbar_wait_bounded(&bar[buf], round & 1, s_abort, a.status);
     ok = __all_sync(kFull, ok);
     if (!ok) break;
-    int64_t s0;
-    int v0, v1;
+    int s0, v0, v1;
     bounds(j, s0, v0, v1);
-    const uint32_t grp = paged ? groups >> (8 * buf) : 3u;
+    const uint32_t grp = groups >> (8 * buf);
     constexpr uint32_t kAll = (1u << (CH / 16)) - 1u;
     const bool whole = v0 == 0 && v1 == CH && (grp & kAll) == kAll;
-    unsigned char* ktile = mine + buf * 2 * C::kTile;
-    unsigned char* vtile = ktile + C::kTile;
     uint32_t see = 0xffffffffu;  // bit i: key i
     if (!whole) {
       see = (v1 >= 32 ? 0xffffffffu : (1u << v1) - 1u) & ~(v0 >= 32 ? 0xffffffffu : (1u << v0) - 1u);
       see &= ((grp & 1u) ? 0xffffu : 0u) | ((grp & 2u) ? 0xffff0000u : 0u);
+      unsigned char* vtile = mine + buf * 2 * C::kTile + C::kTile;
       for (int r = 0; r < CH; ++r)
         if (!((see >> r) & 1u))
           for (int c = lane; c < D * C::EB / 16; c += 32)
@@ -299,7 +303,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2)
       fence_async_smem();  // before the next copy into this buffer
       __syncwarp();
     }
-    const uint32_t kt = smem_u32(ktile), vt = smem_u32(vtile);
+    const uint32_t kt = tiles0 + buf * 2 * C::kTile + k_lane, vt = tiles0 + buf * 2 * C::kTile + C::kTile + v_lane;
 
     // S = Q K^T: even and odd steps apart (shorter chains)
     float s[NT][2];
@@ -315,7 +319,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2)
 #pragma unroll
           for (int i = 0; i < NT; ++i) {
             uint32_t b[4];
-            ldm4(kt + tile_offset(CH, 8 * i + (lane & 7), 4 * u + (lane >> 3)), b);
+            ldm4((kt ^ ((u & 1) * 64)) + (u >> 1) * CH * 128 + i * 1024, b);
             mma_e4m3(sa[i], q8[2 * u], b[0], b[1]);
             mma_e4m3(sb[i], q8[2 * u + 1], b[2], b[3]);
           }
@@ -330,7 +334,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2)
 #pragma unroll
           for (int i = 0; i < NT; ++i) {
             uint32_t b[4];
-            ldm4(kt + tile_offset(CH, 8 * i + (lane & 7), 4 * u + (lane >> 3)), b);
+            ldm4((kt ^ ((u & 1) * 64)) + (u >> 1) * CH * 128 + i * 1024, b);
             mma_bf16(sa[i], qa[2 * u][0], 0u, qa[2 * u][1], 0u, b[0], b[1]);
             mma_bf16(sb[i], qa[2 * u + 1][0], 0u, qa[2 * u + 1][1], 0u, b[2], b[3]);
           }
@@ -348,11 +352,11 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2)
       for (int e = 0; e < 2; ++e) {
         const int key = 8 * i + 2 * qd + e;
         float g = s[i][e] * kLog2e;
-        if (gated && s0 + key != t.p0) {
+        if (gated && s0 + key != p0) {
           if (a.gate == ETA_GATE_HARD) g = s[i][e] >= tau ? g : -INFINITY;
           else g *= row_rcp(1.0f + row_ex2(nbl * (s[i][e] - tau)));
         }
-        if (!((see >> key) & 1u)) g = -INFINITY;
+        if (!whole && !((see >> key) & 1u)) g = -INFINITY;
         s[i][e] = g;
         bm = fmaxf(bm, g);
       }
@@ -380,7 +384,6 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2)
     // O += P V; weights in two parts
 #pragma unroll
     for (int m2 = 0; m2 < NT / 2; ++m2) {
-      const int vrow = 16 * m2 + 8 * ((lane >> 3) & 1) + (lane & 7);
       const float p0 = s[2 * m2][0], p1 = s[2 * m2][1], p2 = s[2 * m2 + 1][0], p3 = s[2 * m2 + 1][1];
       if constexpr (FP8) {
         auto pack = [](float x, float y) {
@@ -394,7 +397,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2)
 #pragma unroll
         for (int g = 0; g < D / 16; g += 2) {
           uint32_t r[4], ev[4], od[4];
-          ldm4_t(vt + tile_offset(CH, vrow, g + (lane >> 4)), r);
+          ldm4_t((vt ^ (g << 4)) + m2 * 2048, r);
           // a register holds two keys x two dims: bytes 0, 2 are the even dim's keys, 1, 3 the odd's
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -416,13 +419,14 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2)
 #pragma unroll
         for (int jd = 0; jd < NDT; jd += 2) {
           uint32_t r[4];
-          ldm4_t(vt + tile_offset(CH, vrow, jd + (lane >> 4)), r);
+          ldm4_t((vt ^ ((jd & 7) << 4)) + (jd >> 3) * CH * 128 + m2 * 2048, r);
           mma_bf16(o[jd], h0, l0, h1, l1, r[0], r[1]);
           mma_bf16(o[jd + 1], h0, l0, h1, l1, r[2], r[3]);
         }
       }
     }
     __syncwarp();  // every lane is done with the buffer
+    if (++buf == kRowBufs) buf = 0, ++round;
   }
   if (!ok && lane == 0) {  // copies in flight land before the block exits
     for (int j = max(0, issued - kRowBufs); j < issued; ++j) {
