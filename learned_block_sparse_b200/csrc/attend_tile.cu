@@ -50,6 +50,7 @@ namespace {
 constexpr int kTileThreads = 384;
 constexpr int kTR = 128;  // rows per query tile
 constexpr int kTK = 128;  // keys per key tile
+constexpr int kHK = 64;   // keys per half of it: a step of the softmax
 
 enum { kNoGate = 0, kSigmoid = 1, kHard = 2 };
 
@@ -81,6 +82,28 @@ __device__ __forceinline__ void e4m3_to_bf16(uint32_t w, uint32_t& lo, uint32_t&
   const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&b));
   lo = pack2(x.x, x.y);
   hi = pack2(y.x, y.y);
+}
+
+// packed pairs of fp32 values
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t p) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 // Bits i of word w (keys 32 w + i) with lo <= key < hi.
@@ -117,13 +140,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   uint64_t* s_full = reinterpret_cast<uint64_t*>(s_kv + NB * L::kTile + L::kRawBufs * L::kRaw);
   uint64_t* s_empty = s_full + NB;
   uint64_t* s_qrdy = s_empty + NB;                // query tiles are in shared memory
-  uint64_t* s_sfull = s_qrdy + 1;                 // [2] logits are in TMEM
-  uint64_t* s_prdy = s_sfull + 2;                 // [2] weights are in TMEM
-  uint64_t* s_ofull = s_prdy + 2;                 // all MMAs are done
+  uint64_t* s_sfull = s_qrdy + 1;                 // [tile][half] logits are in TMEM
+  uint64_t* s_prdy = s_sfull + 4;                 // [tile][half] weights are in TMEM
+  uint64_t* s_pv = s_prdy + 4;                    // [tile] their products are in O
+  uint64_t* s_ofull = s_pv + 2;                   // all MMAs are done
   int* s_abort = reinterpret_cast<int*>(s_ofull + 1);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_abort + 1);
   uint32_t* s_pages = s_tmem + 1;                 // [8] per key tile (mod 8): 16-key groups whose page exists
-  uint64_t* s_rfull = FP8 ? s_ofull + 8 : s_full;   // raw fp8 tiles: landed, converted
+  uint64_t* s_rfull = FP8 ? s_ofull + 7 : s_full;   // raw fp8 tiles: landed, converted
   uint64_t* s_rempty = FP8 ? s_rfull + NR : s_empty;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.y, split = blockIdx.z;
@@ -139,10 +163,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       mbar_init(&s_rfull[i], 1);
       mbar_init(&s_rempty[i], 2);
     }
-    for (int w = 0; w < 2; ++w) {
-      mbar_init(&s_sfull[w], 2);
-      mbar_init(&s_prdy[w], 128);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&s_sfull[i], 2);
+      mbar_init(&s_prdy[i], 128);
     }
+    for (int w = 0; w < 2; ++w) mbar_init(&s_pv[w], 1);
     mbar_init(s_qrdy, 256);
     mbar_init(s_ofull, 1);
     fence_mbar_init();
@@ -201,7 +226,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (warp == 8) tmem_alloc(s_tmem, 512);
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *s_tmem;
+  const uint32_t tmem = *s_tmem;  // 0: the whole of TMEM is this block's
   volatile int* abort_flag = s_abort;
   int armed = 0;  // uses of the ring whose copies were issued (warp 9)
 
@@ -255,65 +280,92 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
     } else if (warp == 8) {
       // ------------------------------------------------------------------ MMAs
-      if (lane == 0) {
-        constexpr uint32_t dS = mma_desc_bf16(kTR, kTK, false), dO = mma_desc_bf16(kTR, D, true);
-        const uint32_t q_addr = smem_u32(s_q), kv_addr = smem_u32(s_kv);
-        bool ok = mbar_wait_bounded(s_qrdy, 0, s_abort, a.status);
-        auto wait_use = [&](int use) {
-          return mbar_wait_bounded(&s_full[use % NB], (use / NB) & 1, s_abort, a.status);
-        };
-        auto logits = [&](int w, int j) {  // S_w = Q_w K_j^T
-          const uint32_t k_addr = kv_addr + static_cast<uint32_t>((2 * j) % NB) * L::kTile;
+      // The whole warp runs this, every value uniform; one lane issues (see elect_lane).
+      // TMEM is allocated whole, so its columns are compile-time constants: S of tile w
+      // at 128 w (64 a half, P over it), O of tile w at 256 + D w.
+      constexpr uint32_t dS = mma_desc_bf16(kTR, kHK, false), dO = mma_desc_bf16(kTR, D, true);
+      const uint32_t q_lo = desc_lo(smem_u32(s_q), 16);
+      const uint32_t k_lo = desc_lo(smem_u32(s_kv), 16), v_lo = desc_lo(smem_u32(s_kv), kTK * 128);
+      auto wait = [&](uint64_t* bar, int parity) {
+        return __all_sync(kFull, mbar_wait_bounded(bar, parity, s_abort, a.status)) != 0;
+      };
+      auto logits = [&](int w, int half, int buf) {  // S = Q_w K^T for a half of the key tile in `buf`
+        if (elect_lane()) {
+          const uint32_t q = q_lo + w * (L::kQ >> 4), k = k_lo + buf * (L::kTile >> 4) + half * (kHK * 128 >> 4);
+          const uint32_t d = w * 128 + half * kHK;
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t off = (ks >> 2) * kTK * 128 + (ks & 3) * 32;
-            mma_f16_ss(tmem + w * 128, smem_desc(q_addr + w * L::kQ + off, 16, 1024), smem_desc(k_addr + off, 16, 1024),
-                       dS, ks > 0);
+            const uint32_t off = ((ks >> 2) * kTK * 128 + (ks & 3) * 32) >> 4;
+            if (ks == 0) mma_f16_ss<false>(d, desc_of(q + off), desc_of(k + off), dS);
+            else mma_f16_ss<true>(d, desc_of(q + off), desc_of(k + off), dS);
           }
-          tc_commit(&s_sfull[w]);
-          mbar_arrive(&s_sfull[w]);  // also publishes what the loads' barrier published (the page mask)
-        };
-        if (ok) ok = n > 0 && wait_use(0);
-        tc_fence_after();
-        if (ok) {
-          for (int w = 0; w < ntiles; ++w) logits(w, 0);
-          tc_commit(&s_empty[0]);
+          tc_commit(&s_sfull[2 * w + half]);
+          mbar_arrive(&s_sfull[2 * w + half]);  // also publishes what the loads' barrier published (the page mask)
         }
-        for (int j = 0; ok && j < n; ++j) {
-          const uint32_t v_addr = kv_addr + static_cast<uint32_t>((2 * j + 1) % NB) * L::kTile;
-          for (int w = 0; w < ntiles; ++w) {
-            ok = mbar_wait_bounded(&s_prdy[w], j & 1, s_abort, a.status) && (w > 0 || wait_use(2 * j + 1));
-            if (!ok) break;
+        __syncwarp();
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (elect_lane()) tc_commit(bar);
+        __syncwarp();
+      };
+      bool ok = wait(s_qrdy, 0) && n > 0 && wait(&s_full[0], 0);
+      tc_fence_after();
+      if (ok) {
+        for (int half = 0; half < 2; ++half)
+          for (int w = 0; w < ntiles; ++w) logits(w, half, 0);
+        commit(&s_empty[0]);
+      }
+      int kb = 2 % NB, kr = 2 / NB, vb = 1 % NB, vr = 1 / NB;  // ring places of K_{j+1}, V_j, and their rounds
+      for (int j = 0; ok && j < n; ++j) {
+        const bool more = j + 1 < n;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            if (w >= ntiles || !ok) continue;
+            ok = wait(&s_prdy[2 * w + half], j & 1);
+            if (ok && w == 0 && half == 0) ok = wait(&s_full[vb], vr & 1);
+            if (!ok) continue;
             tc_fence_after();
-            const uint32_t o = tmem + 256 + w * D, p = tmem + w * 128;
+            if (elect_lane()) {
+              const uint32_t v = v_lo + vb * (L::kTile >> 4) + half * (kHK * 128 >> 4);
+              const uint32_t o = 256 + w * D, p = w * 128 + half * kHK;
+              const uint32_t first = j == 0 && half == 0 ? 0u : 1u;
 #pragma unroll
-            for (int ks = 0; ks < kTK / 16; ++ks)
-              mma_f16_ts(o, p + ks * 8, smem_desc(v_addr + ks * 2048, kTK * 128, 1024), dO, j > 0 || ks > 0);
-            if (HILO) {
+              for (int ks = 0; ks < kHK / 16; ++ks)
+                mma_f16_ts(o, p + ks * 8, desc_of(v + ks * (2048 >> 4)), dO, ks == 0 ? first : 1u);
+              if (HILO) {
 #pragma unroll
-              for (int ks = 0; ks < kTK / 16; ++ks)
-                mma_f16_ts(o, p + 64 + ks * 8, smem_desc(v_addr + ks * 2048, kTK * 128, 1024), dO, true);
+                for (int ks = 0; ks < kHK / 16; ++ks)
+                  mma_f16_ts(o, p + kHK / 2 + ks * 8, desc_of(v + ks * (2048 >> 4)), dO, 1u);
+              }
+              tc_commit(&s_pv[w]);
             }
-            if (w == ntiles - 1) tc_commit(&s_empty[(2 * j + 1) % NB]);
-            if (j + 1 < n) {
-              if (w == 0) {
-                ok = wait_use(2 * j + 2);
-                if (!ok) break;
+            __syncwarp();
+            const bool last = half == 1 && w == ntiles - 1;
+            if (last) commit(&s_empty[vb]);
+            if (more) {
+              if (w == 0 && half == 0) {
+                ok = wait(&s_full[kb], kr & 1);
+                if (!ok) continue;
                 tc_fence_after();
               }
-              logits(w, j + 1);
-              if (w == ntiles - 1) tc_commit(&s_empty[(2 * j + 2) % NB]);
+              logits(w, half, kb);
+              if (last) commit(&s_empty[kb]);
             }
           }
         }
-        tc_commit(s_ofull);  // after the last MMA, or after those issued before an abort
-        if (!ok) {
-          const uint64_t t0 = global_timer_ns();
-          while (!mbar_try_wait(s_ofull, 0) && global_timer_ns() - t0 < kWaitLimitNs) {
-          }
-        }
+        kb += 2, vb += 2;
+        if (kb >= NB) kb -= NB, ++kr;
+        if (vb >= NB) vb -= NB, ++vr;
       }
-      __syncwarp();
+      commit(s_ofull);  // after the last MMA, or after those issued before an abort
+      if (!ok) {
+        const uint64_t t0 = global_timer_ns();
+        while (!mbar_try_wait(s_ofull, 0) && global_timer_ns() - t0 < kWaitLimitNs) {
+        }
+        __syncwarp();
+      }
     } else if (FP8) {
       // ------------------------------------- fp8 tiles to bf16 (warps 10, 11)
       // A thread widens 16-byte pieces (16 keys or values of one row) of every second
@@ -362,91 +414,100 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(warp & 3) << 21);  // lanes 32 (warp % 4) ..
     const uint32_t sp = lane_addr + w * 128, so = lane_addr + 256 + w * D;
     const int64_t tok = t.tok0 + (row >> g_log2);
-    const int64_t qrow = tok * a.Hq + h * G + (row & (G - 1));
-    const float qs = a.qscale;                     // logit = S qs
+    auto q_row = [&](int r_) {                     // row of q (and of the output) of block row r_
+      return (t.tok0 + (r_ >> g_log2)) * a.Hq + h * G + (r_ & (G - 1));
+    };
     {
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + (live ? qrow : 0) * D);
+      // the tile's queries, D / 8 threads per row (coalesced)
+      constexpr int P = D / 8, RPP = 128 / P;
       unsigned char* dst = s_q + w * L::kQ;
-#pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        const uint4 x = live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-        *reinterpret_cast<uint4*>(dst + tile_offset(kTR, r, c)) = x;
+      const int c = r % P;
+#pragma unroll 4
+      for (int i = 0; i < P; ++i) {
+        const int rr = i * RPP + r / P;
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (w * kTR + rr < rows)
+          x = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + q_row(w * kTR + rr) * D) + c);
+        *reinterpret_cast<uint4*>(dst + tile_offset(kTR, rr, c)) = x;
       }
       fence_async_smem();
       mbar_arrive(s_qrdy);
     }
     const int64_t p = t.p0 + (row >> g_log2);      // this row's position (prefix: past every key)
-    const float c2 = qs * kLog2e;
+    const float qs = a.qscale, c2 = qs * kLog2e;   // logit = S qs, in log2 units S c2
     float tau = 0.0f;
     if (GATE != kNoGate && live) tau = a.tau[tok * a.tau_stride + h * G + (row & (G - 1))];
     const float gk = -a.beta * kLog2e * qs, gb = a.beta * kLog2e * tau;
     float m = -INFINITY, l = 0.0f;                 // log2 units
     bool ok = w < ntiles;
-    for (int j = 0; ok && j < n; ++j) {
-      ok = mbar_wait_bounded(&s_sfull[w], j & 1, s_abort, a.status);
+    for (int i = 0; ok && i < 2 * n; ++i) {
+      const int half = i & 1, j = i >> 1;
+      ok = mbar_wait_bounded(&s_sfull[2 * w + half], j & 1, s_abort, a.status);
       ok = __all_sync(kFull, ok);
       if (!ok) break;
       tc_fence_after();
+      const uint32_t sph = sp + half * kHK;
+      float s[kHK];
+      tmem_ld32(sph, reinterpret_cast<uint32_t*>(s));
+      tmem_ld32(sph + 32, reinterpret_cast<uint32_t*>(s) + 32);
       int64_t s0;
       int v0, v1;
       bounds(j, s0, v0, v1);
-      float s[kTK];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) tmem_ld32(sp + 32 * i, reinterpret_cast<uint32_t*>(s) + 32 * i);
-      tc_wait_ld();
       const uint32_t groups = paged ? s_pages[j & 7] : 0xffu;
       // every key visible to every row of the block and none of them a row's own: no checks
       const bool inside = v0 == 0 && v1 == kTK && groups == 0xffu &&
                           (prefix || (s0 + kTK <= t.p0 && (s0 > t.p0 + t.nq - 1 - a.window || s0 + kTK <= a.sinks)));
-      if (GATE == kSigmoid) {
-        const int own = prefix ? -1 : static_cast<int>(min(int64_t{kTK}, p - s0));
+      if (!FP8 && !inside && w == 0 && half == 0) {
+        // thread r owns key r: its V row is zeroed when no query may see it
+        const bool dead = r < v0 || r >= v1 || !((groups >> (r >> 4)) & 1u);
+        if (__any_sync(kFull, dead)) {
+          const int use = 2 * j + 1;
+          ok = mbar_wait_bounded(&s_full[use % NB], (use / NB) & 1, s_abort, a.status);
+          if (ok && dead) {
+            unsigned char* vt = s_kv + static_cast<size_t>(use % NB) * L::kTile;
 #pragma unroll
-        for (int i = 0; i < kTK; ++i) {
-          const float g = s[i] * c2 * rcp(1.0f + ex2(fmaf(s[i], gk, gb)));
-          s[i] = (!inside && i == own) ? s[i] * c2 : g;
+            for (int c = 0; c < D / 8; ++c)
+              *reinterpret_cast<uint4*>(vt + tile_offset(kTK, r, c)) = make_uint4(0u, 0u, 0u, 0u);
+            fence_async_smem();
+          }
+          ok = __all_sync(kFull, ok);
+          if (!ok) break;
+        }
+      }
+      tc_wait_ld();
+      const int64_t sh = s0 + half * kHK;          // first key of the half
+      if (GATE == kSigmoid) {
+        const int own = prefix ? -1 : static_cast<int>(min(int64_t{kHK}, max(int64_t{-1}, p - sh)));
+#pragma unroll
+        for (int k = 0; k < kHK; ++k) {
+          const float g = s[k] * c2 * rcp(1.0f + ex2(fmaf(s[k], gk, gb)));
+          s[k] = (!inside && k == own) ? s[k] * c2 : g;
         }
       } else if (GATE == kHard) {
-        const int own = prefix ? -1 : static_cast<int>(min(int64_t{kTK}, p - s0));
+        const int own = prefix ? -1 : static_cast<int>(min(int64_t{kHK}, max(int64_t{-1}, p - sh)));
 #pragma unroll
-        for (int i = 0; i < kTK; ++i) s[i] = (s[i] * qs >= tau || (!inside && i == own)) ? s[i] * c2 : -INFINITY;
+        for (int k = 0; k < kHK; ++k) s[k] = (s[k] * qs >= tau || (!inside && k == own)) ? s[k] * c2 : -INFINITY;
       }
       if (!inside) {
-        const int64_t up = p - s0 + 1, from = p - a.window + 1 - s0, sk = a.sinks - s0;
+        const int64_t up = p - sh + 1, from = p - a.window + 1 - sh, sk = a.sinks - sh;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t see = range_bits(v0, v1, q);
-          if (!prefix) see &= range_bits(0, up, q) & (range_bits(from, kTK, q) | range_bits(0, sk, q));
-          const uint32_t pg = groups >> (2 * q);
+        for (int q = 0; q < 2; ++q) {
+          uint32_t see = range_bits(v0 - half * kHK, v1 - half * kHK, q);
+          if (!prefix) see &= range_bits(0, up, q) & (range_bits(from, kHK, q) | range_bits(0, sk, q));
+          const uint32_t pg = groups >> (4 * half + 2 * q);
           see &= ((pg & 1u) ? 0xffffu : 0u) | ((pg & 2u) ? 0xffff0000u : 0u);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) s[32 * q + i] = (see >> i) & 1u ? s[32 * q + i] : -INFINITY;
-        }
-        if (!FP8 && w == 0) {
-          // thread r owns key r: its V row is zeroed when no query may see it
-          const bool dead = r < v0 || r >= v1 || !((groups >> (r >> 4)) & 1u);
-          if (__any_sync(kFull, dead)) {
-            const int use = 2 * j + 1;
-            ok = mbar_wait_bounded(&s_full[use % NB], (use / NB) & 1, s_abort, a.status);
-            if (ok && dead) {
-              unsigned char* vt = s_kv + static_cast<size_t>(use % NB) * L::kTile;
-#pragma unroll
-              for (int c = 0; c < D / 8; ++c)
-                *reinterpret_cast<uint4*>(vt + tile_offset(kTK, r, c)) = make_uint4(0u, 0u, 0u, 0u);
-              fence_async_smem();
-            }
-            ok = __all_sync(kFull, ok);
-            if (!ok) break;
-          }
+          for (int k = 0; k < 32; ++k) s[32 * q + k] = (see >> k) & 1u ? s[32 * q + k] : -INFINITY;
         }
       }
       // running maximum (four chains), in log2 units
       float m0 = s[0], m1 = s[1], m2 = s[2], m3 = s[3];
 #pragma unroll
-      for (int i = 4; i < kTK; i += 4) {
-        m0 = fmaxf(m0, s[i]);
-        m1 = fmaxf(m1, s[i + 1]);
-        m2 = fmaxf(m2, s[i + 2]);
-        m3 = fmaxf(m3, s[i + 3]);
+      for (int k = 4; k < kHK; k += 4) {
+        m0 = fmaxf(m0, s[k]);
+        m1 = fmaxf(m1, s[k + 1]);
+        m2 = fmaxf(m2, s[k + 2]);
+        m3 = fmaxf(m3, s[k + 3]);
       }
       float mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
       if (GATE == kNoGate) mx *= c2;
@@ -456,78 +517,100 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const float f = m == mn ? 1.0f : ex2(m - mn);
         l *= f;
         m = mn;
-        if (j > 0) {
+        if (i > 0) {
+          ok = mbar_wait_bounded(&s_pv[w], (i - 1) & 1, s_abort, a.status);  // O is complete up to the last half
+          ok = __all_sync(kFull, ok);
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
+          for (int k = 0; k < D / 32; ++k) {
             float o[32];
-            tmem_ld32(so + 32 * i, reinterpret_cast<uint32_t*>(o));
+            tmem_ld32(so + 32 * k, reinterpret_cast<uint32_t*>(o));
             tc_wait_ld();
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] *= f;
-            tmem_st32(so + 32 * i, reinterpret_cast<const uint32_t*>(o));
+            tmem_st32(so + 32 * k, reinterpret_cast<const uint32_t*>(o));
           }
         }
       }
       const float base = m == -INFINITY ? 0.0f : m;
-      float l0 = 0.0f, l1 = 0.0f, l2 = 0.0f, l3 = 0.0f;
+      // weights: two at a time where the machine has packed fp32 arithmetic
+      const uint64_t scale2 = pair(GATE == kNoGate ? c2 : 1.0f, GATE == kNoGate ? c2 : 1.0f), base2 = pair(-base, -base);
+      uint64_t sum0 = 0, sum1 = 0;
+      uint32_t hi[32], lo[HILO ? 32 : 1];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint32_t hi[32], lo[HILO ? 32 : 1];
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          const int e = 64 * q + 2 * i;
-          float x[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            x[k] = GATE == kNoGate ? ex2(fmaf(s[e + k], c2, -base)) : ex2(s[e + k] - base);
-          l0 += x[0];
-          l1 += x[1];
-          l2 += x[2];
-          l3 += x[3];
-          hi[i] = pack2(x[0], x[1]);
-          hi[i + 1] = pack2(x[2], x[3]);
-          if (HILO) {
-            lo[i] = pack2(x[0] - bf16_lo(hi[i]), x[1] - bf16_hi(hi[i]));
-            lo[i + 1] = pack2(x[2] - bf16_lo(hi[i + 1]), x[3] - bf16_hi(hi[i + 1]));
-          }
+      for (int k = 0; k < 32; k += 2) {
+        const float2 y0 = unpair(fma2(pair(s[2 * k], s[2 * k + 1]), scale2, base2));
+        const float2 y1 = unpair(fma2(pair(s[2 * k + 2], s[2 * k + 3]), scale2, base2));
+        const float x0 = ex2(y0.x), x1 = ex2(y0.y), x2 = ex2(y1.x), x3 = ex2(y1.y);
+        sum0 = add2(sum0, pair(x0, x1));
+        sum1 = add2(sum1, pair(x2, x3));
+        hi[k] = pack2(x0, x1);
+        hi[k + 1] = pack2(x2, x3);
+        if (HILO) {
+          lo[k] = pack2(x0 - bf16_lo(hi[k]), x1 - bf16_hi(hi[k]));
+          lo[k + 1] = pack2(x2 - bf16_lo(hi[k + 1]), x3 - bf16_hi(hi[k + 1]));
         }
-        tmem_st32(sp + 32 * q, hi);
-        if (HILO) tmem_st32(sp + 64 + 32 * q, lo);
       }
-      l += (l0 + l1) + (l2 + l3);
+      tmem_st32(sph, hi);
+      if (HILO) tmem_st32(sph + kHK / 2, lo);
+      const float2 t0 = unpair(sum0), t1 = unpair(sum1);
+      l += (t0.x + t0.y) + (t1.x + t1.y);
       tc_wait_st();
       tc_fence_before();
-      mbar_arrive(&s_prdy[w]);
+      mbar_arrive(&s_prdy[2 * w + half]);
     }
     // -------------------------------------------------------------- epilogue
     if (ok) ok = __all_sync(kFull, mbar_wait_bounded(s_ofull, 0, s_abort, a.status));
     if (ok) {
       tc_fence_after();
       const bool direct = a.o_part == nullptr;
-      const int64_t part = static_cast<int64_t>(prefix ? a.own_splits + split : split) * a.T * a.Hq + qrow;
+      const int64_t part = static_cast<int64_t>(prefix ? a.own_splits + split : split) * a.T * a.Hq;
       const float inv = direct ? (l > 0.0f ? 1.0f / l : 0.0f) : 1.0f;
-      if (live && !direct) a.ml_part[part] = make_float2(m, l);
-      if (n > 0) {
+      if (live && !direct) a.ml_part[part + q_row(row)] = make_float2(m, l);
+      // 128 bytes of every row at a time, through shared memory (the query tiles are
+      // free), so that eight lanes write one row's 128 bytes
+      unsigned char* stage = s_q + warp * 4096;
+      const int row0 = w * kTR + (warp & 3) * 32;
+      auto write = [&](unsigned char* out, int row_bytes, int at) {
+        __syncwarp();
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          float o[32];
-          tmem_ld32(so + 32 * i, reinterpret_cast<uint32_t*>(o));
-          tc_wait_ld();
-          if (!live) continue;
+        for (int k = 0; k < 8; ++k) {
+          const int rr = 4 * k + (lane >> 3), c = lane & 7;
+          const uint4 x = *reinterpret_cast<const uint4*>(stage + tile_offset(32, rr, c));
+          if (row0 + rr < rows) *reinterpret_cast<uint4*>(out + q_row(row0 + rr) * row_bytes + at + 16 * c) = x;
+        }
+        __syncwarp();
+      };
+      if (n > 0 && direct && a.out_dtype == ETA_BF16) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] *= inv;
-          if (direct && a.out_dtype == ETA_BF16) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + qrow * D + 32 * i);
+        for (int k = 0; k < D / 64; ++k) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              dst[e] = make_uint4(pack2(o[8 * e], o[8 * e + 1]), pack2(o[8 * e + 2], o[8 * e + 3]),
-                                  pack2(o[8 * e + 4], o[8 * e + 5]), pack2(o[8 * e + 6], o[8 * e + 7]));
-          } else {
-            float4* dst = reinterpret_cast<float4*>(direct ? static_cast<float*>(a.out) + qrow * D + 32 * i
-                                                           : a.o_part + part * D + 32 * i);
+          for (int q = 0; q < 2; ++q) {
+            float o[32];
+            tmem_ld32(so + 64 * k + 32 * q, reinterpret_cast<uint32_t*>(o));
+            tc_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            for (int e = 0; e < 32; e += 8)
+              *reinterpret_cast<uint4*>(stage + tile_offset(32, lane, 4 * q + e / 8)) =
+                  make_uint4(pack2(o[e] * inv, o[e + 1] * inv), pack2(o[e + 2] * inv, o[e + 3] * inv),
+                             pack2(o[e + 4] * inv, o[e + 5] * inv), pack2(o[e + 6] * inv, o[e + 7] * inv));
           }
+          write(static_cast<unsigned char*>(a.out), D * 2, 128 * k);
+        }
+      } else if (n > 0) {
+        unsigned char* out = direct ? static_cast<unsigned char*>(a.out)
+                                    : reinterpret_cast<unsigned char*>(a.o_part + part * D);
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+          float o[32];
+          tmem_ld32(so + 32 * k, reinterpret_cast<uint32_t*>(o));
+          tc_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(stage + tile_offset(32, lane, e / 4)) =
+                make_float4(o[e] * inv, o[e + 1] * inv, o[e + 2] * inv, o[e + 3] * inv);
+          write(out, D * 4, 128 * k);
         }
       }
       tc_fence_before();

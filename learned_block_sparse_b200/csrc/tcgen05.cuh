@@ -38,27 +38,41 @@ constexpr uint32_t mma_desc_bf16(int M, int N, bool b_mn_major) {
          (static_cast<uint32_t>(M / 16) << 24);
 }
 
-// Shared-memory matrix descriptor, 128-byte swizzle (8-row atoms of 1024 bytes):
-// lead = bytes between 64-element groups along the contiguous dimension (MN-major
-// only), atoms = bytes between atoms of 8 rows.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t atoms) {
-  return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | (static_cast<uint64_t>(lead >> 4) << 16) |
-         (static_cast<uint64_t>(atoms >> 4) << 32) | (1ull << 46) | (2ull << 61);
+// Shared-memory matrix descriptor, 128-byte swizzle (8-row atoms of 1024 bytes). Its
+// upper word is a constant for a given distance of the atoms; the lower one holds the
+// address and `lead`, the bytes between 64-element groups along the contiguous
+// dimension (MN-major only). Both count in 16 bytes, so a step of the matrix is an
+// addition to the lower word.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lead) {
+  return (addr >> 4) | ((lead >> 4) << 16);
+}
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo) { return (static_cast<uint64_t>(kDescHi) << 32) | lo; }
+
+// One lane of a converged warp. The MMA loop runs with the whole warp, its values the
+// same in every lane, and only the instructions themselves under this predicate: the
+// compiler then keeps descriptors in uniform registers. With the loop inside a
+// `lane == 0` branch every MMA first moved its operands over: ~115 cycles an MMA.
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 
-__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
+template <bool ADD>
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(desc), "r"(static_cast<uint32_t>(add))
+      "l"(a), "l"(b), "r"(desc), "n"(ADD ? 1 : 0)
       : "memory");
 }
 // A in TMEM: row r's 16-bit elements 2c, 2c + 1 in column c of lane r.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add) {
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, uint32_t add) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(desc), "r"(static_cast<uint32_t>(add))
+      "r"(a), "l"(b), "r"(desc), "r"(add)
       : "memory");
 }
 
