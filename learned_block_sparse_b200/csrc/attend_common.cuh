@@ -40,6 +40,24 @@ struct AttendArgs {
   float beta, qscale;
 };
 
+// The last row r in [0, B) whose offset satisfies before(r, cu[r]), a condition that
+// holds up to some row (0 if it never does). Whole converged warp, one load a round: the rounds
+// are a dependent chain at the start of every thread block, and 32 probes at once
+// make one of five.
+template <typename Before>
+__device__ __forceinline__ int last_row(const int32_t* cu, int B, Before before) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = B;  // the answer lies in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) >> 5, r = lo + lane * step;
+    const bool yes = lane == 0 || (lane * step < n && before(r, static_cast<int64_t>(__ldg(cu + r))));
+    const int k = 31 - __clz(__ballot_sync(kFull, yes));  // (offsets out of order: still inside)
+    n = min(step, n - k * step);
+    lo += k * step;
+  }
+  return lo;
+}
+
 // One tile of the own pass: nq packed queries of row b from token tok0 on, the
 // first at cache position p0.
 struct OwnTile {
@@ -59,12 +77,7 @@ __device__ __forceinline__ bool own_tile(const AttendArgs& a, int item, int qt_l
       const int64_t c0 = a.cu_q[item], c1 = a.cu_q[item + 1];
       if (c0 < 0 || c1 < c0 || c1 > a.T) atomicExch(a.status, static_cast<int32_t>(ETA_ERR_INVALID_ARG));
     }
-    int lo = 0, hi = a.B - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if ((static_cast<int64_t>(__ldg(a.cu_q + mid)) >> qt_log2) + mid <= item) lo = mid;
-      else hi = mid - 1;
-    }
+    const int lo = last_row(a.cu_q, a.B, [&](int r, int64_t c) { return (c >> qt_log2) + r <= item; });
     t.b = lo;
     first = __ldg(a.cu_q + lo);
     fresh = __ldg(a.cu_q + lo + 1) - first;
@@ -90,12 +103,7 @@ __device__ __forceinline__ bool token_live(const AttendArgs& a, int64_t t) {
   int b = static_cast<int>(t);
   int64_t fresh = 1;
   if (a.cu_q != nullptr) {
-    int lo = 0, hi = a.B - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (__ldg(a.cu_q + mid) <= t) lo = mid;
-      else hi = mid - 1;
-    }
+    const int lo = last_row(a.cu_q, a.B, [&](int, int64_t c) { return c <= t; });
     b = lo;
     const int64_t c0 = __ldg(a.cu_q + b), c1 = __ldg(a.cu_q + b + 1);
     if (c0 < 0 || c1 > a.T || t < c0 || t >= c1) return false;

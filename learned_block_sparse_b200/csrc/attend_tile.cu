@@ -39,6 +39,7 @@
 #include <cuda_fp16.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "attend_common.cuh"
 #include "tcgen05.cuh"
@@ -51,6 +52,10 @@ constexpr int kTileThreads = 384;
 constexpr int kTR = 128;  // rows per query tile
 constexpr int kTK = 128;  // keys per key tile
 constexpr int kHK = 64;   // keys per half of it: a step of the softmax
+
+// Of the pairs of weights with bf16 output, kPoly of 2 kPolyOf are computed on the FMA
+// pipe: the special-function units give one exponential per thread in 8 cycles.
+constexpr int kPoly = 0, kPolyOf = 3;
 
 enum { kNoGate = 0, kSigmoid = 1, kHard = 2 };
 
@@ -106,6 +111,31 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+
+// 2^x of a pair, x <= 127, on the FMA pipe: x = n + f with n the nearest integer (the
+// addition of 1.5 x 2^23 leaves it in the low mantissa bits), 2^f on |f| <= 1/2 by the
+// cubic of least relative error (7.5e-5, fitted by weighted least squares), n added to
+// the exponent. Below 2^-126 the result is 2^-126.
+__device__ __forceinline__ float2 ex2_fma(uint64_t y) {
+  const float2 c = unpair(y);
+  const uint64_t x = pair(fmaxf(c.x, -126.0f), fmaxf(c.y, -126.0f));
+  const uint64_t magic = pair(12582912.0f, 12582912.0f);
+  const uint64_t t = add2(x, magic);
+  const uint64_t n = add2(t, pair(-12582912.0f, -12582912.0f));
+  const uint64_t f = fma2(n, pair(-1.0f, -1.0f), x);
+  uint64_t p = fma2(f, pair(0.0551716685f, 0.0551716685f), pair(0.2426111251f, 0.2426111251f));
+  p = fma2(p, f, pair(0.6932609677f, 0.6932609677f));
+  p = fma2(p, f, pair(0.9999280572f, 0.9999280572f));
+  const float2 u = unpair(t), v = unpair(p);
+  return make_float2(__int_as_float(__float_as_int(v.x) + (__float_as_int(u.x) << 23)),
+                     __int_as_float(__float_as_int(v.y) + (__float_as_int(u.y) << 23)));
+}
+
 // Bits i of word w (keys 32 w + i) with lo <= key < hi.
 __device__ __forceinline__ uint32_t range_bits(int64_t lo, int64_t hi, int w) {
   const int a = static_cast<int>(max(int64_t{0}, min(int64_t{32}, lo - 32 * w)));
@@ -140,14 +170,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   uint64_t* s_full = reinterpret_cast<uint64_t*>(s_kv + NB * L::kTile + L::kRawBufs * L::kRaw);
   uint64_t* s_empty = s_full + NB;
   uint64_t* s_qrdy = s_empty + NB;                // query tiles are in shared memory
-  uint64_t* s_sfull = s_qrdy + 1;                 // [tile][half] logits are in TMEM
-  uint64_t* s_prdy = s_sfull + 4;                 // [tile][half] weights are in TMEM
-  uint64_t* s_pv = s_prdy + 4;                    // [tile] their products are in O
-  uint64_t* s_ofull = s_pv + 2;                   // all MMAs are done
+  uint64_t* s_sfull = s_qrdy + 1;                 // [tile] logits are in TMEM (and O is complete up to the last tile)
+  uint64_t* s_prdy = s_sfull + 2;                 // [tile][half] weights are in TMEM
+  uint64_t* s_ofull = s_prdy + 4;                 // all MMAs are done
   int* s_abort = reinterpret_cast<int*>(s_ofull + 1);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_abort + 1);
   uint32_t* s_pages = s_tmem + 1;                 // [8] per key tile (mod 8): 16-key groups whose page exists
-  uint64_t* s_rfull = FP8 ? s_ofull + 7 : s_full;   // raw fp8 tiles: landed, converted
+  uint64_t* s_rfull = FP8 ? s_ofull + 6 : s_full;   // raw fp8 tiles: landed, converted
   uint64_t* s_rempty = FP8 ? s_rfull + NR : s_empty;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.y, split = blockIdx.z;
@@ -163,11 +192,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       mbar_init(&s_rfull[i], 1);
       mbar_init(&s_rempty[i], 2);
     }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&s_sfull[i], 2);
-      mbar_init(&s_prdy[i], 128);
-    }
-    for (int w = 0; w < 2; ++w) mbar_init(&s_pv[w], 1);
+    for (int w = 0; w < 2; ++w) mbar_init(&s_sfull[w], 2);
+    for (int i = 0; i < 4; ++i) mbar_init(&s_prdy[i], 128);
     mbar_init(s_qrdy, 256);
     mbar_init(s_ofull, 1);
     fence_mbar_init();
@@ -182,7 +208,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int qt_log2 = 8 - g_log2;  // 256 rows
   OwnTile t;
   Visible vis;
-  int64_t tiles, tiles_a = 0;
+  int tiles, tiles_a = 0;
   const int item = static_cast<int>(gridDim.x) - 1 - static_cast<int>(blockIdx.x);  // long causal tiles first
   if (prefix) {
     t.b = 0;
@@ -191,31 +217,32 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     t.p0 = a.P;
     vis.a1 = vis.b0 = 0;
     vis.b1 = a.P;
-    tiles = (a.P + kTK - 1) / kTK;
+    tiles = static_cast<int>((a.P + kTK - 1) / kTK);
   } else {
     if (!own_tile(a, item, qt_log2, tid == 0 && h == 0 && split == 0, t)) return;
     vis = visible_of(a, t.p0, t.p0 + t.nq - 1);
-    tiles_a = (vis.a1 + kTK - 1) / kTK;
+    tiles_a = static_cast<int>((vis.a1 + kTK - 1) / kTK);
   }
   const bool paged = prefix ? a.pblocks != nullptr : a.block_table != nullptr;
   // key tiles of a paged store start on a block: a tile is then 128 / bs whole pages
   const int64_t base_b = paged ? vis.b0 & ~static_cast<int64_t>(a.bs - 1) : vis.b0;
-  if (!prefix) tiles = tiles_a + (vis.b1 - base_b + kTK - 1) / kTK;
-  const int64_t u0 = tiles * split / splits;
-  const int n = static_cast<int>(tiles * (split + 1) / splits - u0);  // key tiles of this block
+  if (!prefix) tiles = tiles_a + static_cast<int>((vis.b1 - base_b + kTK - 1) / kTK);
+  // key tiles [u0, u0 + n) are this block's (fewer than 2^24 tiles, at most 128 splits)
+  const int u0 = static_cast<int>(static_cast<uint32_t>(tiles) * split / splits);
+  const int n = static_cast<int>(static_cast<uint32_t>(tiles) * (split + 1) / splits) - u0;
   const int rows = t.nq << g_log2;
   const int ntiles = rows > kTR ? 2 : 1;
 
   // first key of key tile u0 + j, and the keys [v0, v1) of it that some query may see
   auto bounds = [&](int j, int64_t& s0, int& v0, int& v1) {
-    const int64_t u = u0 + j;
+    const int u = u0 + j;
     int64_t lo, hi;
     if (u < tiles_a) {
-      s0 = u * kTK;
+      s0 = static_cast<int64_t>(u) * kTK;
       lo = 0;
       hi = vis.a1;
     } else {
-      s0 = base_b + (u - tiles_a) * kTK;
+      s0 = base_b + static_cast<int64_t>(u - tiles_a) * kTK;
       lo = vis.b0;
       hi = vis.b1;
     }
@@ -282,25 +309,24 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       // ------------------------------------------------------------------ MMAs
       // The whole warp runs this, every value uniform; one lane issues (see elect_lane).
       // TMEM is allocated whole, so its columns are compile-time constants: S of tile w
-      // at 128 w (64 a half, P over it), O of tile w at 256 + D w.
-      constexpr uint32_t dS = mma_desc_bf16(kTR, kHK, false), dO = mma_desc_bf16(kTR, D, true);
+      // at 128 w (P over it: 64 columns, the remainders in the next 64), O at 256 + D w.
+      constexpr uint32_t dS = mma_desc_bf16(kTR, kTK, false), dO = mma_desc_bf16(kTR, D, true);
       const uint32_t q_lo = desc_lo(smem_u32(s_q), 16);
       const uint32_t k_lo = desc_lo(smem_u32(s_kv), 16), v_lo = desc_lo(smem_u32(s_kv), kTK * 128);
       auto wait = [&](uint64_t* bar, int parity) {
         return __all_sync(kFull, mbar_wait_bounded(bar, parity, s_abort, a.status)) != 0;
       };
-      auto logits = [&](int w, int half, int buf) {  // S = Q_w K^T for a half of the key tile in `buf`
+      auto logits = [&](int w, int buf) {  // S_w = Q_w K^T, K in `buf`
         if (elect_lane()) {
-          const uint32_t q = q_lo + w * (L::kQ >> 4), k = k_lo + buf * (L::kTile >> 4) + half * (kHK * 128 >> 4);
-          const uint32_t d = w * 128 + half * kHK;
+          const uint32_t q = q_lo + w * (L::kQ >> 4), k = k_lo + buf * (L::kTile >> 4), d = w * 128;
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             const uint32_t off = ((ks >> 2) * kTK * 128 + (ks & 3) * 32) >> 4;
             if (ks == 0) mma_f16_ss<false>(d, desc_of(q + off), desc_of(k + off), dS);
             else mma_f16_ss<true>(d, desc_of(q + off), desc_of(k + off), dS);
           }
-          tc_commit(&s_sfull[2 * w + half]);
-          mbar_arrive(&s_sfull[2 * w + half]);  // also publishes what the loads' barrier published (the page mask)
+          tc_commit(&s_sfull[w]);
+          mbar_arrive(&s_sfull[w]);  // also publishes what the loads' barrier published (the page mask)
         }
         __syncwarp();
       };
@@ -311,25 +337,23 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       bool ok = wait(s_qrdy, 0) && n > 0 && wait(&s_full[0], 0);
       tc_fence_after();
       if (ok) {
-        for (int half = 0; half < 2; ++half)
-          for (int w = 0; w < ntiles; ++w) logits(w, half, 0);
+        for (int w = 0; w < ntiles; ++w) logits(w, 0);
         commit(&s_empty[0]);
       }
       int kb = 2 % NB, kr = 2 / NB, vb = 1 % NB, vr = 1 / NB;  // ring places of K_{j+1}, V_j, and their rounds
       for (int j = 0; ok && j < n; ++j) {
-        const bool more = j + 1 < n;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
+        for (int w = 0; w < 2; ++w) {
+          if (w >= ntiles || !ok) continue;
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            if (w >= ntiles || !ok) continue;
-            ok = wait(&s_prdy[2 * w + half], j & 1);
+          for (int half = 0; half < 2; ++half) {
+            ok = ok && wait(&s_prdy[2 * w + half], j & 1);
             if (ok && w == 0 && half == 0) ok = wait(&s_full[vb], vr & 1);
             if (!ok) continue;
             tc_fence_after();
             if (elect_lane()) {
               const uint32_t v = v_lo + vb * (L::kTile >> 4) + half * (kHK * 128 >> 4);
-              const uint32_t o = 256 + w * D, p = w * 128 + half * kHK;
+              const uint32_t o = 256 + w * D, p = w * 128 + half * (kHK / 2);
               const uint32_t first = j == 0 && half == 0 ? 0u : 1u;
 #pragma unroll
               for (int ks = 0; ks < kHK / 16; ++ks)
@@ -337,22 +361,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               if (HILO) {
 #pragma unroll
                 for (int ks = 0; ks < kHK / 16; ++ks)
-                  mma_f16_ts(o, p + kHK / 2 + ks * 8, desc_of(v + ks * (2048 >> 4)), dO, 1u);
+                  mma_f16_ts(o, p + 64 + ks * 8, desc_of(v + ks * (2048 >> 4)), dO, 1u);
               }
-              tc_commit(&s_pv[w]);
             }
             __syncwarp();
-            const bool last = half == 1 && w == ntiles - 1;
-            if (last) commit(&s_empty[vb]);
-            if (more) {
-              if (w == 0 && half == 0) {
-                ok = wait(&s_full[kb], kr & 1);
-                if (!ok) continue;
-                tc_fence_after();
-              }
-              logits(w, half, kb);
-              if (last) commit(&s_empty[kb]);
+          }
+          if (!ok) continue;
+          if (w == ntiles - 1) commit(&s_empty[vb]);
+          if (j + 1 < n) {
+            if (w == 0) {
+              ok = wait(&s_full[kb], kr & 1);
+              if (!ok) continue;
+              tc_fence_after();
             }
+            logits(w, kb);
+            if (w == ntiles - 1) commit(&s_empty[kb]);
           }
         }
         kb += 2, vb += 2;
@@ -422,14 +445,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       constexpr int P = D / 8, RPP = 128 / P;
       unsigned char* dst = s_q + w * L::kQ;
       const int c = r % P;
-#pragma unroll 4
+      uint4 x[P];  // all in flight
+#pragma unroll
       for (int i = 0; i < P; ++i) {
         const int rr = i * RPP + r / P;
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        x[i] = make_uint4(0u, 0u, 0u, 0u);
         if (w * kTR + rr < rows)
-          x = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + q_row(w * kTR + rr) * D) + c);
-        *reinterpret_cast<uint4*>(dst + tile_offset(kTR, rr, c)) = x;
+          x[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + q_row(w * kTR + rr) * D) + c);
       }
+#pragma unroll
+      for (int i = 0; i < P; ++i) *reinterpret_cast<uint4*>(dst + tile_offset(kTR, i * RPP + r / P, c)) = x[i];
       fence_async_smem();
       mbar_arrive(s_qrdy);
     }
@@ -439,25 +464,27 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (GATE != kNoGate && live) tau = a.tau[tok * a.tau_stride + h * G + (row & (G - 1))];
     const float gk = -a.beta * kLog2e * qs, gb = a.beta * kLog2e * tau;
     float m = -INFINITY, l = 0.0f;                 // log2 units
+    // key tiles [j_lo, j_hi): every key visible to every row and none of them a row's
+    // own, so nothing is checked (if all their pages exist)
+    const int64_t all_lo = prefix ? 0 : max(vis.b0, t.p0 + t.nq - a.window);
+    const int64_t all_hi = prefix ? a.P : t.p0;
+    const int j_lo = static_cast<int>(tiles_a + (all_lo - base_b + kTK - 1) / kTK - u0);
+    const int j_hi = static_cast<int>(tiles_a + (all_hi - base_b) / kTK - u0);
     bool ok = w < ntiles;
-    for (int i = 0; ok && i < 2 * n; ++i) {
-      const int half = i & 1, j = i >> 1;
-      ok = mbar_wait_bounded(&s_sfull[2 * w + half], j & 1, s_abort, a.status);
+    for (int j = 0; ok && j < n; ++j) {
+      ok = mbar_wait_bounded(&s_sfull[w], j & 1, s_abort, a.status);
       ok = __all_sync(kFull, ok);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t sph = sp + half * kHK;
-      float s[kHK];
-      tmem_ld32(sph, reinterpret_cast<uint32_t*>(s));
-      tmem_ld32(sph + 32, reinterpret_cast<uint32_t*>(s) + 32);
-      int64_t s0;
-      int v0, v1;
-      bounds(j, s0, v0, v1);
+      float s[kTK];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tmem_ld32(sp + 32 * q, reinterpret_cast<uint32_t*>(s) + 32 * q);
       const uint32_t groups = paged ? s_pages[j & 7] : 0xffu;
-      // every key visible to every row of the block and none of them a row's own: no checks
-      const bool inside = v0 == 0 && v1 == kTK && groups == 0xffu &&
-                          (prefix || (s0 + kTK <= t.p0 && (s0 > t.p0 + t.nq - 1 - a.window || s0 + kTK <= a.sinks)));
-      if (!FP8 && !inside && w == 0 && half == 0) {
+      const bool inside = j >= max(j_lo, 0) && j < j_hi && groups == 0xffu && (prefix || u0 + j >= tiles_a);
+      int64_t s0 = 0;
+      int v0 = 0, v1 = kTK;
+      if (!inside) bounds(j, s0, v0, v1);
+      if (!FP8 && !inside && w == 0) {
         // thread r owns key r: its V row is zeroed when no query may see it
         const bool dead = r < v0 || r >= v1 || !((groups >> (r >> 4)) & 1u);
         if (__any_sync(kFull, dead)) {
@@ -475,26 +502,25 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
       }
       tc_wait_ld();
-      const int64_t sh = s0 + half * kHK;          // first key of the half
       if (GATE == kSigmoid) {
-        const int own = prefix ? -1 : static_cast<int>(min(int64_t{kHK}, max(int64_t{-1}, p - sh)));
+        const int own = prefix ? -1 : static_cast<int>(min(int64_t{kTK}, max(int64_t{-1}, p - s0)));
 #pragma unroll
-        for (int k = 0; k < kHK; ++k) {
+        for (int k = 0; k < kTK; ++k) {
           const float g = s[k] * c2 * rcp(1.0f + ex2(fmaf(s[k], gk, gb)));
           s[k] = (!inside && k == own) ? s[k] * c2 : g;
         }
       } else if (GATE == kHard) {
-        const int own = prefix ? -1 : static_cast<int>(min(int64_t{kHK}, max(int64_t{-1}, p - sh)));
+        const int own = prefix ? -1 : static_cast<int>(min(int64_t{kTK}, max(int64_t{-1}, p - s0)));
 #pragma unroll
-        for (int k = 0; k < kHK; ++k) s[k] = (s[k] * qs >= tau || (!inside && k == own)) ? s[k] * c2 : -INFINITY;
+        for (int k = 0; k < kTK; ++k) s[k] = (s[k] * qs >= tau || (!inside && k == own)) ? s[k] * c2 : -INFINITY;
       }
       if (!inside) {
-        const int64_t up = p - sh + 1, from = p - a.window + 1 - sh, sk = a.sinks - sh;
+        const int64_t up = p - s0 + 1, from = p - a.window + 1 - s0, sk = a.sinks - s0;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t see = range_bits(v0 - half * kHK, v1 - half * kHK, q);
-          if (!prefix) see &= range_bits(0, up, q) & (range_bits(from, kHK, q) | range_bits(0, sk, q));
-          const uint32_t pg = groups >> (4 * half + 2 * q);
+        for (int q = 0; q < 4; ++q) {
+          uint32_t see = range_bits(v0, v1, q);
+          if (!prefix) see &= range_bits(0, up, q) & (range_bits(from, kTK, q) | range_bits(0, sk, q));
+          const uint32_t pg = groups >> (2 * q);
           see &= ((pg & 1u) ? 0xffffu : 0u) | ((pg & 2u) ? 0xffff0000u : 0u);
 #pragma unroll
           for (int k = 0; k < 32; ++k) s[32 * q + k] = (see >> k) & 1u ? s[32 * q + k] : -INFINITY;
@@ -503,13 +529,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       // running maximum (four chains), in log2 units
       float m0 = s[0], m1 = s[1], m2 = s[2], m3 = s[3];
 #pragma unroll
-      for (int k = 4; k < kHK; k += 4) {
-        m0 = fmaxf(m0, s[k]);
-        m1 = fmaxf(m1, s[k + 1]);
-        m2 = fmaxf(m2, s[k + 2]);
-        m3 = fmaxf(m3, s[k + 3]);
+      for (int k = 4; k + 8 <= kTK; k += 8) {
+        m0 = max3(m0, s[k], s[k + 1]);
+        m1 = max3(m1, s[k + 2], s[k + 3]);
+        m2 = max3(m2, s[k + 4], s[k + 5]);
+        m3 = max3(m3, s[k + 6], s[k + 7]);
       }
-      float mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+      m0 = max3(m0, s[kTK - 4], s[kTK - 3]);
+      m1 = max3(m1, s[kTK - 2], s[kTK - 1]);
+      float mx = fmaxf(max3(m0, m1, m2), m3);
       if (GATE == kNoGate) mx *= c2;
       const bool grow = mx > m + 8.0f;  // (also the first visible key: m is -inf until then)
       if (__any_sync(kFull, grow)) {
@@ -517,11 +545,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const float f = m == mn ? 1.0f : ex2(m - mn);
         l *= f;
         m = mn;
-        if (i > 0) {
-          ok = mbar_wait_bounded(&s_pv[w], (i - 1) & 1, s_abort, a.status);  // O is complete up to the last half
-          ok = __all_sync(kFull, ok);
-          if (!ok) break;
-          tc_fence_after();
+        if (j > 0) {  // (the MMAs of the last key tile are done: the barrier that released S follows them)
 #pragma unroll
           for (int k = 0; k < D / 32; ++k) {
             float o[32];
@@ -534,31 +558,53 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
       }
       const float base = m == -INFINITY ? 0.0f : m;
-      // weights: two at a time where the machine has packed fp32 arithmetic
+      // weights, in pairs (packed fp32 arithmetic); the first half's products start
+      // while the second is computed
       const uint64_t scale2 = pair(GATE == kNoGate ? c2 : 1.0f, GATE == kNoGate ? c2 : 1.0f), base2 = pair(-base, -base);
       uint64_t sum0 = 0, sum1 = 0;
-      uint32_t hi[32], lo[HILO ? 32 : 1];
+      auto weights = [&](int half, auto some_on_fma) {
+        constexpr bool fma_pipe = decltype(some_on_fma)::value;
+        uint32_t hi[32], lo[HILO ? 32 : 1];
 #pragma unroll
-      for (int k = 0; k < 32; k += 2) {
-        const float2 y0 = unpair(fma2(pair(s[2 * k], s[2 * k + 1]), scale2, base2));
-        const float2 y1 = unpair(fma2(pair(s[2 * k + 2], s[2 * k + 3]), scale2, base2));
-        const float x0 = ex2(y0.x), x1 = ex2(y0.y), x2 = ex2(y1.x), x3 = ex2(y1.y);
-        sum0 = add2(sum0, pair(x0, x1));
-        sum1 = add2(sum1, pair(x2, x3));
-        hi[k] = pack2(x0, x1);
-        hi[k + 1] = pack2(x2, x3);
-        if (HILO) {
-          lo[k] = pack2(x0 - bf16_lo(hi[k]), x1 - bf16_hi(hi[k]));
-          lo[k + 1] = pack2(x2 - bf16_lo(hi[k + 1]), x3 - bf16_hi(hi[k + 1]));
+        for (int k = 0; k < 32; k += 2) {
+          const float* e = s + half * kHK + 2 * k;
+          const uint64_t y0 = fma2(pair(e[0], e[1]), scale2, base2);
+          const uint64_t y1 = fma2(pair(e[2], e[3]), scale2, base2);
+          const float2 z0 = unpair(y0), z1 = unpair(y1);
+          float x0, x1, x2, x3;
+          if (fma_pipe && (k >> 1) % kPolyOf < kPoly) {
+            const float2 z = ex2_fma(y0);
+            x0 = z.x;
+            x1 = z.y;
+          } else {
+            x0 = ex2(z0.x);
+            x1 = ex2(z0.y);
+          }
+          x2 = ex2(z1.x);
+          x3 = ex2(z1.y);
+          sum0 = add2(sum0, pair(x0, x1));
+          sum1 = add2(sum1, pair(x2, x3));
+          hi[k] = pack2(x0, x1);
+          hi[k + 1] = pack2(x2, x3);
+          if (HILO) {
+            lo[k] = pack2(x0 - bf16_lo(hi[k]), x1 - bf16_hi(hi[k]));
+            lo[k + 1] = pack2(x2 - bf16_lo(hi[k + 1]), x3 - bf16_hi(hi[k + 1]));
+          }
         }
+        tmem_st32(sp + half * 32, hi);
+        if (HILO) tmem_st32(sp + 64 + half * 32, lo);
+        tc_wait_st();
+        tc_fence_before();
+        mbar_arrive(&s_prdy[2 * w + half]);
+      };
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        // (a hidden key's weight is exactly zero: only where none is hidden may it come from the FMA pipe)
+        if (!HILO && GATE != kHard && inside) weights(half, std::true_type{});
+        else weights(half, std::false_type{});
       }
-      tmem_st32(sph, hi);
-      if (HILO) tmem_st32(sph + kHK / 2, lo);
       const float2 t0 = unpair(sum0), t1 = unpair(sum1);
       l += (t0.x + t0.y) + (t1.x + t1.y);
-      tc_wait_st();
-      tc_fence_before();
-      mbar_arrive(&s_prdy[2 * w + half]);
     }
     // -------------------------------------------------------------- epilogue
     if (ok) ok = __all_sync(kFull, mbar_wait_bounded(s_ofull, 0, s_abort, a.status));
@@ -568,49 +614,40 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const int64_t part = static_cast<int64_t>(prefix ? a.own_splits + split : split) * a.T * a.Hq;
       const float inv = direct ? (l > 0.0f ? 1.0f / l : 0.0f) : 1.0f;
       if (live && !direct) a.ml_part[part + q_row(row)] = make_float2(m, l);
-      // 128 bytes of every row at a time, through shared memory (the query tiles are
-      // free), so that eight lanes write one row's 128 bytes
-      unsigned char* stage = s_q + warp * 4096;
+      // Through shared memory (query tiles and ring are free), 128 bytes of 32 rows a
+      // slab, so that eight lanes write one row's 128 bytes.
+      const bool narrow = direct && a.out_dtype == ETA_BF16;
+      unsigned char* stage = s_q + warp * (D / 32) * 4096;
       const int row0 = w * kTR + (warp & 3) * 32;
-      auto write = [&](unsigned char* out, int row_bytes, int at) {
+      if (n > 0) {
+        float o[D];
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) tmem_ld32(so + 32 * k, reinterpret_cast<uint32_t*>(o) + 32 * k);
+        tc_wait_ld();
+        if (narrow) {
+#pragma unroll
+          for (int e = 0; e < D; e += 8)
+            *reinterpret_cast<uint4*>(stage + (e >> 6) * 4096 + tile_offset(32, lane, (e >> 3) & 7)) =
+                make_uint4(pack2(o[e] * inv, o[e + 1] * inv), pack2(o[e + 2] * inv, o[e + 3] * inv),
+                           pack2(o[e + 4] * inv, o[e + 5] * inv), pack2(o[e + 6] * inv, o[e + 7] * inv));
+        } else {
+#pragma unroll
+          for (int e = 0; e < D; e += 4)
+            *reinterpret_cast<float4*>(stage + (e >> 5) * 4096 + tile_offset(32, lane, (e >> 2) & 7)) =
+                make_float4(o[e] * inv, o[e + 1] * inv, o[e + 2] * inv, o[e + 3] * inv);
+        }
         __syncwarp();
+        unsigned char* out = direct ? static_cast<unsigned char*>(a.out)
+                                    : reinterpret_cast<unsigned char*>(a.o_part + part * D);
+        const int slabs = narrow ? D / 64 : D / 32;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const int rr = 4 * k + (lane >> 3), c = lane & 7;
-          const uint4 x = *reinterpret_cast<const uint4*>(stage + tile_offset(32, rr, c));
-          if (row0 + rr < rows) *reinterpret_cast<uint4*>(out + q_row(row0 + rr) * row_bytes + at + 16 * c) = x;
-        }
-        __syncwarp();
-      };
-      if (n > 0 && direct && a.out_dtype == ETA_BF16) {
-#pragma unroll
-        for (int k = 0; k < D / 64; ++k) {
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            float o[32];
-            tmem_ld32(so + 64 * k + 32 * q, reinterpret_cast<uint32_t*>(o));
-            tc_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              *reinterpret_cast<uint4*>(stage + tile_offset(32, lane, 4 * q + e / 8)) =
-                  make_uint4(pack2(o[e] * inv, o[e + 1] * inv), pack2(o[e + 2] * inv, o[e + 3] * inv),
-                             pack2(o[e + 4] * inv, o[e + 5] * inv), pack2(o[e + 6] * inv, o[e + 7] * inv));
-          }
-          write(static_cast<unsigned char*>(a.out), D * 2, 128 * k);
-        }
-      } else if (n > 0) {
-        unsigned char* out = direct ? static_cast<unsigned char*>(a.out)
-                                    : reinterpret_cast<unsigned char*>(a.o_part + part * D);
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k) {
-          float o[32];
-          tmem_ld32(so + 32 * k, reinterpret_cast<uint32_t*>(o));
-          tc_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4*>(stage + tile_offset(32, lane, e / 4)) =
-                make_float4(o[e] * inv, o[e + 1] * inv, o[e + 2] * inv, o[e + 3] * inv);
-          write(out, D * 4, 128 * k);
+          if (row0 + rr >= rows) continue;
+          unsigned char* dst = out + q_row(row0 + rr) * (slabs * 128) + 16 * c;
+          for (int q = 0; q < slabs; ++q)
+            *reinterpret_cast<uint4*>(dst + 128 * q) =
+                *reinterpret_cast<const uint4*>(stage + q * 4096 + tile_offset(32, rr, c));
         }
       }
       tc_fence_before();
