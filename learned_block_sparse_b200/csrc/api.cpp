@@ -296,6 +296,8 @@ eta_status_t check_predictor(const eta_shape_t* s, const void* q, const float* W
   return ETA_OK;
 }
 
+constexpr int64_t kPositionSlack = 4096;
+
 // A packed list of new tokens: one per row without cu.
 eta_status_t check_new(const eta_shape_t* s, const int32_t* cu, int64_t n_new) {
   if (n_new < 0 || n_new > INT32_MAX) return ETA_ERR_INVALID_ARG;
@@ -326,7 +328,8 @@ eta_status_t make_attend(const eta_shape_t* s, const eta_params_t* p, const eta_
   if (pages != nullptr) ETA_TRY(check_pages(*pages));
   ETA_TRY(check_store_rows(s, pages != nullptr ? pages->num_pages : 0));
   if (static_cast<int64_t>(s->batch) * s->n_kv_heads > kMaxBH) return ETA_ERR_UNSUPPORTED;
-  if (in->n_new * s->n_q_heads > INT32_MAX) return ETA_ERR_UNSUPPORTED;
+  // token x head rows, and positions up to a tile past a row's end, are 32-bit integers in the kernels
+  if (in->n_new * s->n_q_heads > INT32_MAX || s->capacity > INT32_MAX - kPositionSlack) return ETA_ERR_UNSUPPORTED;
   if (ws == nullptr || !aligned(ws, 256) || ws_bytes < attend_workspace_bytes(*s, in->n_new, with_prefix))
     return ETA_ERR_WORKSPACE;
   std::memset(c, 0, sizeof(*c));
@@ -735,6 +738,7 @@ ETA_API eta_status_t eta_attend_shared(const eta_shape_t* shape, const eta_param
                                        const void* v, const eta_pages_t* pages, const int32_t* seq_lens,
                                        int64_t n_tokens, void* workspace, size_t ws_bytes, eta_stream_t stream) {
   if (prefix == nullptr || prefix->n_tokens < 0 || prefix->n_tokens > INT32_MAX) return ETA_ERR_INVALID_ARG;
+  if (prefix->n_tokens > INT32_MAX - kPositionSlack) return ETA_ERR_UNSUPPORTED;
   AttendCall c;
   ETA_TRY(make_attend(shape, params, queries, k, v, pages, seq_lens, n_tokens, workspace, ws_bytes, true, &c));
   if (prefix->n_tokens > 0) {

@@ -6,41 +6,57 @@ namespace eta {
 
 namespace {
 
-// One warp per (token, head): the slots' partials, added in slot order with the
-// weights 2^(m_s - max m); bytes: slots x (D + 2) x 4 read per row.
+constexpr int kMaxSlots = 256;  // own and prefix splits, 128 each at most
+
+// One thread block of D threads per (token, head), thread = coordinate: the slots'
+// partials, added in slot order with the weights 2^(m_s - max m); bytes: slots x
+// (D + 2) x 4 read per row, eight slots in flight.
 template <int D>
-__global__ void __launch_bounds__(256) attend_merge_kernel(const AttendArgs a) {
+__global__ void __launch_bounds__(D) attend_merge_kernel(const AttendArgs a) {
   grid_dependency_wait();
   allow_dependent_launch();
-  const int64_t rows = a.T * a.Hq;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= rows || !token_live(a, row / a.Hq)) return;
+  __shared__ float s_w[kMaxSlots];  // a slot's weight (0: a range without a visible key)
+  __shared__ float s_inv;
+  const int64_t rows = a.T * a.Hq, row = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (!token_live(a, row / a.Hq)) return;
   const int slots = a.own_splits + a.prefix_splits;
-  float M = -INFINITY;
-  for (int s = lane; s < slots; s += 32) M = fmaxf(M, a.ml_part[s * rows + row].x);
+  if (tid < 32) {
+    float M = -INFINITY, L = 0.0f;
+    for (int s = lane; s < slots; s += 32) M = fmaxf(M, a.ml_part[s * rows + row].x);
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-  constexpr int V = D / 32;
-  float o[V], L = 0.0f;
+    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+    for (int s = lane; s < slots; s += 32) {
+      const float2 ml = a.ml_part[s * rows + row];
+      const float w = ml.y > 0.0f ? exp2f(ml.x - M) : 0.0f;
+      s_w[s] = w;
+      L = fmaf(w, ml.y, L);
+    }
 #pragma unroll
-  for (int i = 0; i < V; ++i) o[i] = 0.0f;
-  for (int s = 0; s < slots; ++s) {
-    const float2 ml = a.ml_part[s * rows + row];
-    if (!(ml.y > 0.0f)) continue;  // a range without a visible key
-    const float c = exp2f(ml.x - M);
-    L = fmaf(c, ml.y, L);
-    const float* p = a.o_part + (s * rows + row) * D + lane;
-#pragma unroll
-    for (int i = 0; i < V; ++i) o[i] = fmaf(c, p[32 * i], o[i]);
+    for (int o = 16; o >= 1; o >>= 1) L += __shfl_xor_sync(kFull, L, o);
+    if (lane == 0) s_inv = L > 0.0f ? 1.0f / L : 0.0f;
   }
-  const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+  const float* p = a.o_part + row * D + tid;
+  const int64_t step = rows * D;
+  float o = 0.0f;
+  bool ready = false;
+  for (int s = 0; s < slots; s += 8) {
+    float x[8];
 #pragma unroll
-  for (int i = 0; i < V; ++i) store_out(a.out, a.out_dtype, row * D + lane + 32 * i, o[i] * inv);
+    for (int i = 0; i < 8; ++i)
+      if (s + i < slots) x[i] = p[(s + i) * step];
+    if (!ready) __syncthreads();  // the weights, while the first partials are on their way
+    ready = true;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (s + i < slots && s_w[s + i] > 0.0f) o = fmaf(s_w[s + i], x[i], o);  // (an empty range wrote nothing)
+  }
+  store_out(a.out, a.out_dtype, row * D + tid, o * s_inv);
 }
 
 enum Kernel { kSimt, kTile, kRow };
 
+constexpr int kMaxSplits = 128;
 constexpr int kRowWant = 10;  // thread blocks per SM that a kRow pass is split into
 
 // A pass: its kernel and its splits.
@@ -66,7 +82,7 @@ Pass pass_of(const eta_shape_t& s, int64_t T, bool prefix, bool single, int64_t 
     p.splits = clamp_splits((kRowWant * sms + items - 1) / items, keys / 64);
   else                         // about four thread blocks per SM
     p.splits = clamp_splits((4 * sms + items - 1) / items, (keys + 31) / 32);
-  if (p.splits > 128) p.splits = 128;
+  if (p.splits > kMaxSplits) p.splits = kMaxSplits;
   return p;
 }
 
@@ -111,11 +127,15 @@ cudaError_t launch_attend(const AttendCall& c, cudaStream_t st) {
     if (p.kernel == kRow) return launch_attend_row(a, c.shape.kv_dtype, D, st);
     return launch_attend_simt(a, c.shape.kv_dtype, D, prefix, st);
   };
-  if (a.P > 0) e = launch(pre, true);
+  if (a.P > 0) {
+    e = launch(pre, true);
+    a.beside = 1;
+  }
   if (e == cudaSuccess) e = launch(own, false);
   if (e != cudaSuccess || slots == 1) return e;
-  return D == 128 ? launch_pdl(attend_merge_kernel<128>, static_cast<unsigned>((a.T * a.Hq + 7) / 8), 256u, 0, st, a)
-                  : launch_pdl(attend_merge_kernel<64>, static_cast<unsigned>((a.T * a.Hq + 7) / 8), 256u, 0, st, a);
+  const unsigned rows = static_cast<unsigned>(a.T * a.Hq);
+  return D == 128 ? launch_pdl(attend_merge_kernel<128>, rows, 128u, 0, st, a)
+                  : launch_pdl(attend_merge_kernel<64>, rows, 64u, 0, st, a);
 }
 
 }  // namespace eta

@@ -37,8 +37,23 @@ struct AttendArgs {
   int64_t T, n, cap, nb_cap, pcap, P, window, sinks, tau_stride;
   int B, Hq, Hkv, G, bs, bs_log2, num_pages, q_dtype, out_dtype, gate;
   int own_splits, prefix_splits;  // slots: the own pass's, then the prefix pass's
+  int beside;  // an own pass that runs beside the prefix pass launched before it: see start_pass
   float beta, qscale;
 };
+
+// Every pass begins with start_pass and ends, on each path, with end_pass (any one
+// thread). A pass normally waits for the kernel before it on the stream. The own pass
+// of a shared-prefix call needs nothing of the prefix pass before it, and that pass
+// lets its dependents start only once it has itself waited: everything older is then
+// complete. So `beside` waits at its end instead (the merge after it waits for this
+// pass alone), and the two run together as far as the SMs have room.
+__device__ __forceinline__ void start_pass(const AttendArgs& a, bool prefix) {
+  if (prefix || !a.beside) grid_dependency_wait();
+  allow_dependent_launch();
+}
+__device__ __forceinline__ void end_pass(const AttendArgs& a, bool prefix) {
+  if (!prefix && a.beside) grid_dependency_wait();
+}
 
 // The last row r in [0, B) whose offset satisfies before(r, cu[r]), a condition that
 // holds up to some row (0 if it never does). Whole converged warp, one load a round: the rounds
@@ -68,27 +83,21 @@ struct OwnTile {
 // Tile `item` of the own pass, 2^qt_log2 queries per tile. Row b's tiles take the
 // items from floor(cu[b] / QT) + b on: ceil(n_b / QT) of them, which is at most
 // the distance to the next row's first, so no prefix sum is needed (items in
-// between are empty). False: nothing to do.
-__device__ __forceinline__ bool own_tile(const AttendArgs& a, int item, int qt_log2, bool report, OwnTile& t) {
+// between are empty). False: nothing to do; *bad: and the row's values are invalid.
+__device__ __forceinline__ bool own_tile_of(const AttendArgs& a, int item, int row, int qt_log2, OwnTile& t, bool* bad) {
   int64_t fresh = 1, first = item, j = 0;
-  t.b = item;
+  t.b = row;
   if (a.cu_q != nullptr) {
-    if (report && item < a.B) {  // every row's bounds are looked at once
-      const int64_t c0 = a.cu_q[item], c1 = a.cu_q[item + 1];
-      if (c0 < 0 || c1 < c0 || c1 > a.T) atomicExch(a.status, static_cast<int32_t>(ETA_ERR_INVALID_ARG));
-    }
-    const int lo = last_row(a.cu_q, a.B, [&](int r, int64_t c) { return (c >> qt_log2) + r <= item; });
-    t.b = lo;
-    first = __ldg(a.cu_q + lo);
-    fresh = __ldg(a.cu_q + lo + 1) - first;
+    first = __ldg(a.cu_q + row);
+    fresh = __ldg(a.cu_q + row + 1) - first;
     if (first < 0 || fresh <= 0 || first + fresh > a.T) return false;
-    j = item - ((first >> qt_log2) + lo);
+    j = item - ((first >> qt_log2) + row);
     if (j < 0 || (j << qt_log2) >= fresh) return false;
   }
-  const int64_t len = a.seq_lens != nullptr ? static_cast<int64_t>(__ldg(a.seq_lens + t.b)) : a.n;
+  const int64_t len = a.seq_lens != nullptr ? static_cast<int64_t>(__ldg(a.seq_lens + row)) : a.n;
   if (len == 0 && a.cu_q == nullptr) return false;  // an idle row
   if (len < fresh || len > a.n) {
-    if (report) atomicExch(a.status, static_cast<int32_t>(ETA_ERR_INVALID_ARG));
+    *bad = true;
     return false;
   }
   const int64_t q0 = j << qt_log2;
@@ -96,6 +105,32 @@ __device__ __forceinline__ bool own_tile(const AttendArgs& a, int item, int qt_l
   t.nq = static_cast<int>(min(fresh - q0, int64_t{1} << qt_log2));
   t.p0 = len - fresh + q0;
   return true;
+}
+// The same for a whole converged warp; `report`: record invalid values.
+__device__ __forceinline__ bool own_tile(const AttendArgs& a, int item, int qt_log2, bool report, OwnTile& t) {
+  int row = item;
+  if (a.cu_q != nullptr) {
+    if (report && item < a.B) {  // every row's bounds are looked at once
+      const int64_t c0 = a.cu_q[item], c1 = a.cu_q[item + 1];
+      if (c0 < 0 || c1 < c0 || c1 > a.T) atomicExch(a.status, static_cast<int32_t>(ETA_ERR_INVALID_ARG));
+    }
+    row = last_row(a.cu_q, a.B, [&](int r, int64_t c) { return (c >> qt_log2) + r <= item; });
+  }
+  bool bad = false;
+  const bool ok = own_tile_of(a, item, row, qt_log2, t, &bad);
+  if (bad && report) atomicExch(a.status, static_cast<int32_t>(ETA_ERR_INVALID_ARG));
+  return ok;
+}
+// And for one thread, of packed queries.
+__device__ __forceinline__ bool own_tile_at(const AttendArgs& a, int item, int qt_log2, OwnTile& t) {
+  int lo = 0, hi = a.cu_q != nullptr ? a.B - 1 : 0;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if ((static_cast<int64_t>(__ldg(a.cu_q + mid)) >> qt_log2) + mid <= item) lo = mid;
+    else hi = mid - 1;
+  }
+  bool bad = false;
+  return own_tile_of(a, item, a.cu_q != nullptr ? lo : item, qt_log2, t, &bad);
 }
 
 // Whether packed token t belongs to a row whose queries the own pass computes.
@@ -191,6 +226,7 @@ inline AttendArgs make_attend_args(const AttendCall& c) {
   a.out_dtype = c.in.out_dtype;
   a.gate = c.gate;
   a.own_splits = a.prefix_splits = 1;
+  a.beside = 0;
   a.beta = c.beta;
   a.qscale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(s.head_dim)));
   return a;

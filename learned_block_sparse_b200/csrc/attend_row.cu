@@ -129,10 +129,12 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowBlocks)
     for (int i = 0; i < kRowWarps * kRowBufs; ++i) mbar_init(&s_bar[i], 1);
     fence_mbar_init();
   }
-  grid_dependency_wait();
-  allow_dependent_launch();
+  start_pass(a, false);
   OwnTile t;
-  if (!own_tile(a, blockIdx.x, 0, tid == 0 && h == 0 && split == 0, t)) return;
+  if (!own_tile(a, blockIdx.x, 0, tid == 0 && h == 0 && split == 0, t)) {
+    end_pass(a, false);
+    return;
+  }
   // positions, chunks and store rows of a call fit in 32 bits (the host checks the rows)
   const Visible vis = visible_of(a, t.p0, t.p0);
   const int p0 = static_cast<int>(t.p0), a1 = static_cast<int>(vis.a1), b0 = static_cast<int>(vis.b0);
@@ -461,7 +463,10 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowBlocks)
     }
   }
   __syncthreads();
-  if (*reinterpret_cast<volatile int*>(s_abort)) return;
+  if (*reinterpret_cast<volatile int*>(s_abort)) {
+    end_pass(a, false);
+    return;
+  }
   const bool direct = a.o_part == nullptr;
   for (int idx = tid; idx < G * D; idx += kRowWarps * 32) {
     const int g = idx / D, e = idx % D;
@@ -484,6 +489,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowBlocks)
       if (e == 0) a.ml_part[part] = make_float2(M, L);
     }
   }
+  end_pass(a, false);
 }
 
 template <int D, int G, bool FP8>

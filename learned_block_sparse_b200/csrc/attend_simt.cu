@@ -46,8 +46,7 @@ __global__ void __launch_bounds__(kThr) attend_simt_kernel(const AttendArgs a) {
   __shared__ int s_ok[kKT];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.y, G = a.G;
-  grid_dependency_wait();
-  allow_dependent_launch();
+  start_pass(a, PREFIX);
 
   const int qt = kR / G;  // queries per tile (a power of two)
   int qt_log2 = 0;
@@ -65,7 +64,10 @@ __global__ void __launch_bounds__(kThr) attend_simt_kernel(const AttendArgs a) {
     vis.b1 = a.P;
     tiles = (a.P + kKT - 1) / kKT;
   } else {
-    if (!own_tile(a, blockIdx.x, qt_log2, tid == 0 && h == 0 && split == 0, t)) return;
+    if (!own_tile(a, blockIdx.x, qt_log2, tid == 0 && h == 0 && split == 0, t)) {
+      end_pass(a, PREFIX);
+      return;
+    }
     vis = visible_of(a, t.p0, t.p0 + t.nq - 1);
     tiles_a = (vis.a1 + kKT - 1) / kKT;
     tiles = tiles_a + (vis.b1 - vis.b0 + kKT - 1) / kKT;
@@ -243,6 +245,7 @@ __global__ void __launch_bounds__(kThr) attend_simt_kernel(const AttendArgs a) {
       else a.o_part[(slot * a.T * a.Hq + row) * D + col] = o;
     }
   }
+  end_pass(a, PREFIX);
 }
 
 template <typename KV, int D>

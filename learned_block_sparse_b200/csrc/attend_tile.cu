@@ -179,7 +179,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   uint64_t* s_rfull = FP8 ? s_ofull + 6 : s_full;   // raw fp8 tiles: landed, converted
   uint64_t* s_rempty = FP8 ? s_rfull + NR : s_empty;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int h = blockIdx.y, split = blockIdx.z;
+  int h = blockIdx.y;
+  const int split = blockIdx.z;
   const int splits = prefix ? a.prefix_splits : a.own_splits;
 
   if (tid == 0) {
@@ -198,8 +199,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     mbar_init(s_ofull, 1);
     fence_mbar_init();
   }
-  grid_dependency_wait();
-  allow_dependent_launch();
+  start_pass(a, prefix != 0);
 
   // this thread block's queries and keys
   const int G = a.G;
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   OwnTile t;
   Visible vis;
   int tiles, tiles_a = 0;
-  const int item = static_cast<int>(gridDim.x) - 1 - static_cast<int>(blockIdx.x);  // long causal tiles first
+  int item = blockIdx.x;
   if (prefix) {
     t.b = 0;
     t.tok0 = static_cast<int64_t>(item) << qt_log2;
@@ -219,7 +219,33 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     vis.b1 = a.P;
     tiles = static_cast<int>((a.P + kTK - 1) / kTK);
   } else {
-    if (!own_tile(a, item, qt_log2, tid == 0 && h == 0 && split == 0, t)) return;
+    if (gridDim.x * gridDim.y > gridDim.z * 148 && gridDim.x <= kTileThreads) {
+      // Longest tiles first, all their heads together: with ~4 tiles per SM the last
+      // ones decide (a chunk behind 8 caches: 280 -> XXX us). Thread i counts tile i's keys.
+      uint32_t* keys = reinterpret_cast<uint32_t*>(tile_smem);
+      const int order = (blockIdx.y * gridDim.x + blockIdx.x) / gridDim.y;
+      h = (blockIdx.y * gridDim.x + blockIdx.x) % gridDim.y;
+      OwnTile mine;
+      uint32_t count = 0;
+      if (tid < static_cast<int>(gridDim.x) && own_tile_at(a, tid, qt_log2, mine)) {
+        const Visible v = visible_of(a, mine.p0, mine.p0 + mine.nq - 1);
+        count = static_cast<uint32_t>(v.a1 + v.b1 - v.b0);
+      }
+      if (tid < static_cast<int>(gridDim.x)) keys[tid] = count;
+      __syncthreads();
+      if (tid < static_cast<int>(gridDim.x)) {
+        int before = 0;
+        for (int i = 0; i < static_cast<int>(gridDim.x); ++i) before += keys[i] > count || (keys[i] == count && i < tid);
+        if (before == order) *reinterpret_cast<volatile int*>(s_tmem) = tid;
+      }
+      __syncthreads();
+      item = *reinterpret_cast<volatile int*>(s_tmem);
+      __syncthreads();
+    }
+    if (!own_tile(a, item, qt_log2, tid == 0 && h == 0 && split == 0, t)) {
+      end_pass(a, false);
+      return;
+    }
     vis = visible_of(a, t.p0, t.p0 + t.nq - 1);
     tiles_a = static_cast<int>((vis.a1 + kTK - 1) / kTK);
   }
@@ -666,6 +692,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tc_fence_after();
     tmem_free(tmem, 512);
   }
+  end_pass(a, prefix != 0);
 }
 
 template <int D, int GATE, bool HILO, bool FP8>
