@@ -54,10 +54,10 @@ __global__ void __launch_bounds__(D) attend_merge_kernel(const AttendArgs a) {
   store_out(a.out, a.out_dtype, row * D + tid, o * s_inv);
 }
 
-enum Kernel { kSimt, kTile, kRow };
+enum Kernel { kSimt, kTile, kRow, kStream };
 
 constexpr int kMaxSplits = 128;
-constexpr int kRowWant = 10;  // thread blocks per SM that a kRow pass is split into
+constexpr int kRowWant = 10;  // thread blocks per SM that a kRow or kStream pass is split into
 
 // A pass: its kernel and its splits.
 struct Pass {
@@ -73,12 +73,12 @@ Pass pass_of(const eta_shape_t& s, int64_t T, bool prefix, bool single, int64_t 
   const int64_t G = s.n_q_heads / s.n_kv_heads, sms = device_sm_count();
   Pass p;
   const bool mma = s.kv_dtype == ETA_FP8_E4M3 || (s.kv_dtype == ETA_BF16 && s.q_dtype == ETA_BF16);
-  p.kernel = !mma ? kSimt : (!prefix && single ? kRow : kTile);
+  p.kernel = !prefix && single ? (mma ? kRow : kStream) : (mma ? kTile : kSimt);
   const int64_t qt = (p.kernel == kTile ? kTileRows : kSimtRows) / G;
   const int64_t items = (prefix ? (T + qt - 1) / qt : (single ? s.batch : T / qt + s.batch)) * s.n_kv_heads;
   if (p.kernel == kTile)       // one thread block per SM, in one wave
     p.splits = clamp_splits(sms / items, prefix ? keys / 128 : keys / 256);
-  else if (p.kernel == kRow)   // two thread blocks per SM, five waves (the last one is rarely full); 64 keys at least
+  else if (p.kernel != kSimt)  // three thread blocks per SM, three waves (the last one is rarely full); 64 keys at least
     p.splits = clamp_splits((kRowWant * sms + items - 1) / items, keys / 64);
   else                         // about four thread blocks per SM
     p.splits = clamp_splits((4 * sms + items - 1) / items, (keys + 31) / 32);
@@ -92,7 +92,7 @@ size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Partial rows (splits x query rows) the passes of a call of up to T queries can
 // leave: at most R (want + items) with splits <= want / items + 1 and R rows per
-// item (kSimt, kRow: R = G), at most R want with splits <= want / items (kTile), never below the
+// item (kSimt; kRow, kStream: R = G), at most R want with splits <= want / items (kTile), never below the
 // query rows when there are two passes. A single pass that is not split leaves
 // none. Non-decreasing in T.
 size_t attend_workspace_bytes(const eta_shape_t& s, int64_t T, bool with_prefix) {
@@ -125,6 +125,7 @@ cudaError_t launch_attend(const AttendCall& c, cudaStream_t st) {
   auto launch = [&](const Pass& p, bool prefix) {
     if (p.kernel == kTile) return launch_attend_tile(a, c.shape.kv_dtype, D, prefix, st);
     if (p.kernel == kRow) return launch_attend_row(a, c.shape.kv_dtype, D, st);
+    if (p.kernel == kStream) return launch_attend_stream(a, c.shape.kv_dtype, D, st);
     return launch_attend_simt(a, c.shape.kv_dtype, D, prefix, st);
   };
   if (a.P > 0) {

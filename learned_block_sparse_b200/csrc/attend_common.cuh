@@ -37,6 +37,7 @@ struct AttendArgs {
   int64_t T, n, cap, nb_cap, pcap, P, window, sinks, tau_stride;
   int B, Hq, Hkv, G, bs, bs_log2, num_pages, q_dtype, out_dtype, gate;
   int own_splits, prefix_splits;  // slots: the own pass's, then the prefix pass's
+  int longest_first;  // attend_tile_kernel's own pass: tiles in order of their keys
   int beside;  // an own pass that runs beside the prefix pass launched before it: see start_pass
   float beta, qscale;
 };
@@ -226,7 +227,7 @@ inline AttendArgs make_attend_args(const AttendCall& c) {
   a.out_dtype = c.in.out_dtype;
   a.gate = c.gate;
   a.own_splits = a.prefix_splits = 1;
-  a.beside = 0;
+  a.beside = a.longest_first = 0;
   a.beta = c.beta;
   a.qscale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(s.head_dim)));
   return a;
@@ -236,6 +237,7 @@ inline AttendArgs make_attend_args(const AttendCall& c) {
 cudaError_t launch_attend_simt(const AttendArgs& a, int kv_dtype, int D, bool prefix, cudaStream_t st);
 cudaError_t launch_attend_tile(const AttendArgs& a, int kv_dtype, int D, bool prefix, cudaStream_t st);
 cudaError_t launch_attend_row(const AttendArgs& a, int kv_dtype, int D, cudaStream_t st);  // own pass, one token per row
+cudaError_t launch_attend_stream(const AttendArgs& a, int kv_dtype, int D, cudaStream_t st);  // the same in fp32
 constexpr int kSimtRows = 16;   // query rows per thread block of attend_simt_kernel
 constexpr int kTileRows = 256;  // of attend_tile_kernel
 

@@ -60,15 +60,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// D[16x8] += A[16x32] B[32x8], e4m3 operands
-__device__ __forceinline__ void mma_e4m3(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 __device__ __forceinline__ float row_ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -87,22 +78,10 @@ __device__ __forceinline__ void widen_e4m3(uint32_t w, uint32_t& lo, uint32_t& h
       : "=r"(lo), "=r"(hi)
       : "r"(w));
 }
-__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-// Four values below 256 -> e4m3 words with v = hi + lo / 16: eight significant bits,
-// all that a bf16 value has (those under 2^-6 of the largest lose their last ones:
-// at most 2^-21 of it).
-__device__ __forceinline__ void split_e4m3(const float (&v)[4], uint32_t& hi, uint32_t& lo) {
-  hi = e4m3_pair(v[0], v[1]) | (e4m3_pair(v[2], v[3]) << 16);
-  uint32_t a, b;
-  widen_e4m3(hi, a, b);
-  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a));
-  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&b));
-  lo = e4m3_pair((v[0] - x.x) * 16.0f, (v[1] - x.y) * 16.0f) |
-       (e4m3_pair((v[2] - y.x) * 16.0f, (v[3] - y.y) * 16.0f) << 16);
+// two fp32 -> packed f16
+__device__ __forceinline__ uint32_t half_pair(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 template <int D, bool FP8>
@@ -211,29 +190,21 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowBlocks)
   const bool live = row < G;
   const int64_t qrow = t.tok0 * a.Hq + h * G + (live ? row : 0);
   const uint16_t* qp = static_cast<const uint16_t*>(a.q) + qrow * D;
-  uint32_t qa[FP8 ? 1 : KST][2];
-  uint32_t q8[FP8 ? 4 : 1][4];
+  uint32_t qa[KST][2];
   float scale = a.qscale;
   if constexpr (FP8) {
-    // this thread's dims of k32 step kk: 32 kk + 4 qd + i, then 16 more; scaled by a
-    // power of two so that the head's largest lies in [128, 256)
-    float x[4][2][4];
+    // f16 queries, exact for bf16 once scaled by a power of two so that the head's largest
+    // lies in [128, 256). Of step kk this thread holds coordinates 16 kk + 4 qd .. + 3 (an
+    // order of its own within the step, which is the order in which a piece of four key
+    // bytes widens).
     float amax = 0.0f;
+    uint2 x[KST];
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const uint2 u = *reinterpret_cast<const uint2*>(qp + 32 * kk + 16 * e + 4 * qd);
-        x[kk][e][0] = bf16_lo(u.x);
-        x[kk][e][1] = bf16_hi(u.x);
-        x[kk][e][2] = bf16_lo(u.y);
-        x[kk][e][3] = bf16_hi(u.y);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (!live) x[kk][e][i] = 0.0f;
-          amax = fmaxf(amax, fabsf(x[kk][e][i]));
-        }
-      }
+    for (int kk = 0; kk < KST; ++kk) {
+      x[kk] = *reinterpret_cast<const uint2*>(qp + 16 * kk + 4 * qd);
+      amax = fmaxf(fmaxf(amax, fmaxf(fabsf(bf16_lo(x[kk].x)), fabsf(bf16_hi(x[kk].x)))),
+                   fmaxf(fabsf(bf16_lo(x[kk].y)), fabsf(bf16_hi(x[kk].y))));
+    }
     amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
     const int E = (__float_as_int(amax) >> 23) & 0xff;
@@ -241,14 +212,9 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowBlocks)
     const float up = __int_as_float((127 + e2) << 23);
     scale *= __int_as_float((127 - e2) << 23);
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[kk][e][i] *= up;
-      }
-      split_e4m3(x[kk][0], q8[kk][0], q8[kk][1]);
-      split_e4m3(x[kk][1], q8[kk][2], q8[kk][3]);
+    for (int kk = 0; kk < KST; ++kk) {
+      qa[kk][0] = live ? half_pair(bf16_lo(x[kk].x) * up, bf16_hi(x[kk].x) * up) : 0u;
+      qa[kk][1] = live ? half_pair(bf16_lo(x[kk].y) * up, bf16_hi(x[kk].y) * up) : 0u;
     }
   } else {
 #pragma unroll
@@ -315,36 +281,29 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowBlocks)
       for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) sa[i][e] = sb[i][e] = 0.0f;
-      if constexpr (FP8) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < D * C::EB / 64; ++u)
 #pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            uint32_t b[4];
-            ldm4((kt ^ ((u & 1) * 64)) + (u >> 1) * CH * 128 + i * 1024, b);
-            mma_e4m3(sa[i], q8[2 * u], b[0], b[1]);
-            mma_e4m3(sb[i], q8[2 * u + 1], b[2], b[3]);
-          }
+        for (int i = 0; i < NT; ++i) {
+          uint32_t b[4];
+          ldm4((kt ^ ((u & 1) * 64)) + (u >> 1) * CH * 128 + i * 1024, b);
+          if constexpr (FP8) {  // a register: four coordinates of a key, one step
+            uint32_t lo[4], hi[4];
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            s[i][e] = fmaf(sa[i][2 + e] + sb[i][2 + e], 0.0625f, sa[i][e] + sb[i][e]) * scale;
-      } else {
-#pragma unroll
-        for (int u = 0; u < KST / 2; ++u)
-#pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            uint32_t b[4];
-            ldm4((kt ^ ((u & 1) * 64)) + (u >> 1) * CH * 128 + i * 1024, b);
+            for (int e = 0; e < 4; ++e) widen_e4m3(b[e], lo[e], hi[e]);
+            mma_f16(sa[i], qa[4 * u][0], 0u, qa[4 * u][1], 0u, lo[0], hi[0]);
+            mma_f16(sb[i], qa[4 * u + 1][0], 0u, qa[4 * u + 1][1], 0u, lo[1], hi[1]);
+            mma_f16(sa[i], qa[4 * u + 2][0], 0u, qa[4 * u + 2][1], 0u, lo[2], hi[2]);
+            mma_f16(sb[i], qa[4 * u + 3][0], 0u, qa[4 * u + 3][1], 0u, lo[3], hi[3]);
+          } else {
             mma_bf16(sa[i], qa[2 * u][0], 0u, qa[2 * u][1], 0u, b[0], b[1]);
             mma_bf16(sb[i], qa[2 * u + 1][0], 0u, qa[2 * u + 1][1], 0u, b[2], b[3]);
           }
+        }
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
+      for (int i = 0; i < NT; ++i)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) s[i][e] = (sa[i][e] + sb[i][e]) * scale;
-      }
+        for (int e = 0; e < 2; ++e) s[i][e] = (sa[i][e] + sb[i][e]) * scale;
     }
     // gate, mask, running maximum of this thread's row
     float bm = -INFINITY;
@@ -388,14 +347,10 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowBlocks)
     for (int m2 = 0; m2 < NT / 2; ++m2) {
       const float p0 = s[2 * m2][0], p1 = s[2 * m2][1], p2 = s[2 * m2 + 1][0], p3 = s[2 * m2 + 1][1];
       if constexpr (FP8) {
-        auto pack = [](float x, float y) {
-          const __half2 v = __floats2half2_rn(x, y);
-          return *reinterpret_cast<const uint32_t*>(&v);
-        };
-        const uint32_t h0 = pack(p0, p1), h1 = pack(p2, p3);
+        const uint32_t h0 = half_pair(p0, p1), h1 = half_pair(p2, p3);
         const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
         const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
-        const uint32_t l0 = pack(p0 - f0.x, p1 - f0.y), l1 = pack(p2 - f1.x, p3 - f1.y);
+        const uint32_t l0 = half_pair(p0 - f0.x, p1 - f0.y), l1 = half_pair(p2 - f1.x, p3 - f1.y);
 #pragma unroll
         for (int g = 0; g < D / 16; g += 2) {
           uint32_t r[4], ev[4], od[4];

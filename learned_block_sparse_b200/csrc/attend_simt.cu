@@ -1,6 +1,6 @@
-// Attention of new tokens on the CUDA cores, in fp32 throughout: any cache and
-// query type, any tile. It serves the fp32 caches (and fp32 queries), whose
-// results keep fp32 precision; bf16 and fp8 caches have the tensor-core kernels.
+// Attention of new tokens on the CUDA cores, in fp32 throughout, for the fp32 caches
+// (and bf16 caches under fp32 queries), whose results keep fp32 precision: packed
+// queries of a row, and the queries of all rows against a shared prefix.
 //
 // One thread block takes 16 tile rows (queries x the G heads of a group) over a
 // range of 32-key tiles. Keys and values are widened to fp32 in shared memory
@@ -20,15 +20,6 @@ namespace eta {
 namespace {
 
 constexpr int kThr = 256, kKT = 32, kR = kSimtRows;  // threads, keys per tile, rows per tile
-
-template <typename KV>
-__device__ __forceinline__ void widen_piece(const uint4& w, float* x) { widen16<KV>(w, x); }
-template <>
-__device__ __forceinline__ void widen_piece<Fp8Raw>(const uint4& w, float* x) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = e4m3_to_float((u[i >> 2] >> (8 * (i & 3))) & 0xffu);
-}
 
 template <typename KV, int D, bool PREFIX>
 __global__ void __launch_bounds__(kThr) attend_simt_kernel(const AttendArgs a) {
@@ -135,7 +126,7 @@ __global__ void __launch_bounds__(kThr) attend_simt_kernel(const AttendArgs a) {
       const int idx = tid + i * kThr;
       const int which = idx / (kKT * CPR), key = (idx / CPR) % kKT, c = idx % CPR;
       float x[EPP];
-      widen_piece<KV>(piece[i], x);
+      widen16<KV>(piece[i], x);
       float* dst = (which == 0 ? s_k : s_v) + key * LD + c * EPP;
 #pragma unroll
       for (int e = 0; e < EPP; e += 4)
@@ -268,7 +259,6 @@ cudaError_t launch_simt_t(const AttendArgs& a, bool prefix, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_attend_simt(const AttendArgs& a, int kv_dtype, int D, bool prefix, cudaStream_t st) {
-  if (kv_dtype == ETA_FP8_E4M3) return launch_simt_t<Fp8Raw, 128>(a, prefix, st);
   if (kv_dtype == ETA_BF16)
     return D == 128 ? launch_simt_t<Bf16Raw, 128>(a, prefix, st) : launch_simt_t<Bf16Raw, 64>(a, prefix, st);
   return D == 128 ? launch_simt_t<float, 128>(a, prefix, st) : launch_simt_t<float, 64>(a, prefix, st);

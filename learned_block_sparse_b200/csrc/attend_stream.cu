@@ -1,0 +1,207 @@
+// Attention of one new token per row in fp32 throughout, for fp32 caches (and bf16
+// caches under fp32 queries): a stream of the row's visible keys on the CUDA cores.
+//
+// Bound: HBM. Nothing is staged: D * bytes / 16 lanes own a key, each lane holds 16
+// bytes of it and the matching coordinates of the query and of the output; the dot
+// product is a butterfly over those lanes, the products with V need none. A warp has
+// kLoads loads of K and of V in flight (8 KB), twelve or more warps share an SM.
+// Groups of lanes, warps and thread blocks each keep their own running maximum, sum
+// and output, added at the end in a fixed order.
+#include "attend_common.cuh"
+
+namespace eta {
+
+namespace {
+
+constexpr int kStreamWarps = 4, kLoads = 8;
+
+template <typename KV, int D, int G>
+__global__ void __launch_bounds__(kStreamWarps * 32) attend_stream_kernel(const AttendArgs a) {
+  constexpr int EB = KvTraits<KV>::kBytes;
+  constexpr int E = 16 / EB;            // coordinates per lane
+  constexpr int LPK = D / E;            // lanes per key
+  constexpr int KPL = 32 / LPK;         // keys per load of the warp
+  constexpr int CH = kLoads * KPL;      // keys per chunk
+  constexpr int kStates = kStreamWarps * KPL;
+  __shared__ __align__(16) float s_o[kStates * G * D];
+  __shared__ float s_ml[kStates * G * 2];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int sub = lane / LPK, at = lane % LPK;
+  const int h = blockIdx.y, split = blockIdx.z, splits = a.own_splits;
+  start_pass(a, false);
+  OwnTile t;
+  if (!own_tile(a, blockIdx.x, 0, tid == 0 && h == 0 && split == 0, t)) {
+    end_pass(a, false);
+    return;
+  }
+  // positions and store rows fit in 32 bits
+  const Visible vis = visible_of(a, t.p0, t.p0);
+  const int p0 = static_cast<int>(t.p0), a1 = static_cast<int>(vis.a1), b0 = static_cast<int>(vis.b0);
+  const int chunks_a = (a1 + CH - 1) / CH, chunks = chunks_a + (p0 + CH - b0) / CH;
+  const int c0 = static_cast<int>(static_cast<int64_t>(chunks) * split / splits);
+  const int c1 = static_cast<int>(static_cast<int64_t>(chunks) * (split + 1) / splits);
+
+  float q[G][E], o[G][E], m[G], l[G], tau[G];
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const int64_t row = t.tok0 * a.Hq + h * G + g;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      q[g][e] = load_elem(a.q, a.q_dtype, row * D + at * E + e) * a.qscale;
+      o[g][e] = 0.0f;
+    }
+    m[g] = -INFINITY;
+    l[g] = 0.0f;
+    tau[g] = a.tau != nullptr ? a.tau[t.tok0 * a.tau_stride + h * G + g] : 0.0f;
+  }
+  const int32_t* table =
+      a.block_table != nullptr ? a.block_table + static_cast<int64_t>(t.b) * a.nb_cap : nullptr;
+  const int seg_row = static_cast<int>((static_cast<int64_t>(t.b) * a.Hkv + h) * a.cap);
+
+  for (int c = c0 + warp; c < c1; c += kStreamWarps) {
+    const int s0 = c < chunks_a ? c * CH : b0 + (c - chunks_a) * CH;
+    const int end = c < chunks_a ? a1 : p0 + 1;
+    uint4 kx[kLoads], vx[kLoads];
+    uint32_t see = 0;  // bit i: this lane's key of load i is visible
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int s = s0 + i * KPL + sub;
+      kx[i] = vx[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (s >= end) continue;
+      int row = seg_row + s;
+      if (table != nullptr) {
+        const int page = __ldg(table + (s >> a.bs_log2));
+        if (page < 0 || page >= a.num_pages) {
+          atomicExch(a.status, static_cast<int32_t>(ETA_ERR_INVALID_ARG));
+          continue;
+        }
+        row = (page * a.Hkv + h) * a.bs + (s & (a.bs - 1));
+      }
+      const int64_t off = static_cast<int64_t>(row) * D * EB + at * 16;
+      kx[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(a.k) + off));
+      vx[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(a.v) + off));
+      see |= 1u << i;
+    }
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      float S[kLoads];
+      float mx = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        float x[E];
+        widen16<KV>(kx[i], x);
+        float d0 = 0.0f, d1 = 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          d0 = fmaf(q[g][e], x[e], d0);
+          d1 = fmaf(q[g][e + 1], x[e + 1], d1);
+        }
+        S[i] = d0 + d1;
+      }
+#pragma unroll
+      for (int w = LPK / 2; w >= 1; w >>= 1)
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) S[i] += __shfl_xor_sync(kFull, S[i], w);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        float v = S[i];
+        if (a.tau != nullptr && s0 + i * KPL + sub != p0) {
+          if (a.gate == ETA_GATE_HARD) v = v >= tau[g] ? v : -INFINITY;
+          else v = v / (1.0f + expf(-a.beta * (v - tau[g])));
+        }
+        S[i] = (see >> i) & 1u ? v * kLog2e : -INFINITY;
+        mx = fmaxf(mx, S[i]);
+      }
+      const float mn = fmaxf(m[g], mx);
+      const float base = mn == -INFINITY ? 0.0f : mn;
+      const float corr = mn == -INFINITY ? 1.0f : exp2f(m[g] - mn);
+      m[g] = mn;
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        S[i] = exp2f(S[i] - base);
+        sum += S[i];
+      }
+      l[g] = fmaf(l[g], corr, sum);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[g][e] *= corr;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        float x[E];
+        widen16<KV>(vx[i], x);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[g][e] = fmaf(S[i], x[e], o[g][e]);
+      }
+    }
+  }
+
+  const int state = warp * KPL + sub;
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+#pragma unroll
+    for (int e = 0; e < E; e += 4)
+      *reinterpret_cast<float4*>(s_o + (state * G + g) * D + at * E + e) =
+          make_float4(o[g][e], o[g][e + 1], o[g][e + 2], o[g][e + 3]);
+    if (at == 0) {
+      s_ml[(state * G + g) * 2] = m[g];
+      s_ml[(state * G + g) * 2 + 1] = l[g];
+    }
+  }
+  __syncthreads();
+  const bool direct = a.o_part == nullptr;
+  for (int idx = tid; idx < G * D; idx += kStreamWarps * 32) {
+    const int g = idx / D, e = idx % D;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kStates; ++w) M = fmaxf(M, s_ml[(w * G + g) * 2]);
+    float ov = 0.0f, L = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kStates; ++w) {
+      const float f = M == -INFINITY ? 0.0f : exp2f(s_ml[(w * G + g) * 2] - M);
+      ov = fmaf(f, s_o[(w * G + g) * D + e], ov);
+      L = fmaf(f, s_ml[(w * G + g) * 2 + 1], L);
+    }
+    const int64_t out_row = t.tok0 * a.Hq + h * G + g;
+    if (direct) {
+      store_out(a.out, a.out_dtype, out_row * D + e, L > 0.0f ? ov / L : 0.0f);
+    } else {
+      const int64_t part = static_cast<int64_t>(split) * a.T * a.Hq + out_row;
+      a.o_part[part * D + e] = ov;
+      if (e == 0) a.ml_part[part] = make_float2(M, L);
+    }
+  }
+  end_pass(a, false);
+}
+
+template <typename KV, int D, int G>
+cudaError_t launch_stream_t(const AttendArgs& a, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.B), static_cast<unsigned>(a.Hkv), static_cast<unsigned>(a.own_splits));
+  cfg.blockDim = dim3(kStreamWarps * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1] = {pdl_attribute()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, attend_stream_kernel<KV, D, G>, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <typename KV, int D>
+cudaError_t launch_stream_g(const AttendArgs& a, cudaStream_t st) {
+  switch (a.G) {
+    case 1: return launch_stream_t<KV, D, 1>(a, st);
+    case 2: return launch_stream_t<KV, D, 2>(a, st);
+    case 4: return launch_stream_t<KV, D, 4>(a, st);
+    default: return launch_stream_t<KV, D, 8>(a, st);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_attend_stream(const AttendArgs& a, int kv_dtype, int D, cudaStream_t st) {
+  if (kv_dtype == ETA_BF16)
+    return D == 128 ? launch_stream_g<Bf16Raw, 128>(a, st) : launch_stream_g<Bf16Raw, 64>(a, st);
+  return D == 128 ? launch_stream_g<float, 128>(a, st) : launch_stream_g<float, 64>(a, st);
+}
+
+}  // namespace eta

@@ -39,7 +39,6 @@
 #include <cuda_fp16.h>
 
 #include <atomic>
-#include <type_traits>
 
 #include "attend_common.cuh"
 #include "tcgen05.cuh"
@@ -52,10 +51,6 @@ constexpr int kTileThreads = 384;
 constexpr int kTR = 128;  // rows per query tile
 constexpr int kTK = 128;  // keys per key tile
 constexpr int kHK = 64;   // keys per half of it: a step of the softmax
-
-// Of the pairs of weights with bf16 output, kPoly of 2 kPolyOf are computed on the FMA
-// pipe: the special-function units give one exponential per thread in 8 cycles.
-constexpr int kPoly = 0, kPolyOf = 3;
 
 enum { kNoGate = 0, kSigmoid = 1, kHard = 2 };
 
@@ -117,23 +112,41 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
   return r;
 }
 
-// 2^x of a pair, x <= 127, on the FMA pipe: x = n + f with n the nearest integer (the
+// 2^x of a pair, |x| <= 126, on the FMA pipe: x = n + f with n the nearest integer (the
 // addition of 1.5 x 2^23 leaves it in the low mantissa bits), 2^f on |f| <= 1/2 by the
-// cubic of least relative error (7.5e-5, fitted by weighted least squares), n added to
-// the exponent. Below 2^-126 the result is 2^-126.
-__device__ __forceinline__ float2 ex2_fma(uint64_t y) {
-  const float2 c = unpair(y);
-  const uint64_t x = pair(fmaxf(c.x, -126.0f), fmaxf(c.y, -126.0f));
-  const uint64_t magic = pair(12582912.0f, 12582912.0f);
-  const uint64_t t = add2(x, magic);
+// quartic of least relative error (2.7e-6, fitted by weighted least squares), n added
+// to the exponent.
+__device__ __forceinline__ float2 ex2_fma(uint64_t x) {
+  const uint64_t t = add2(x, pair(12582912.0f, 12582912.0f));
   const uint64_t n = add2(t, pair(-12582912.0f, -12582912.0f));
   const uint64_t f = fma2(n, pair(-1.0f, -1.0f), x);
-  uint64_t p = fma2(f, pair(0.0551716685f, 0.0551716685f), pair(0.2426111251f, 0.2426111251f));
-  p = fma2(p, f, pair(0.6932609677f, 0.6932609677f));
-  p = fma2(p, f, pair(0.9999280572f, 0.9999280572f));
+  uint64_t p = fma2(f, pair(0.0095701022f, 0.0095701022f), pair(0.0559178591f, 0.0559178591f));
+  p = fma2(p, f, pair(0.2402474433f, 0.2402474433f));
+  p = fma2(p, f, pair(0.6931217909f, 0.6931217909f));
+  p = fma2(p, f, pair(0.9999992847f, 0.9999992847f));
   const float2 u = unpair(t), v = unpair(p);
   return make_float2(__int_as_float(__float_as_int(v.x) + (__float_as_int(u.x) << 23)),
                      __int_as_float(__float_as_int(v.y) + (__float_as_int(u.y) << 23)));
+}
+
+// The gate of two logits, in log2 units: s c / (1 + 2^(s k + b)). The special-function
+// units bound a gated tile (each logit would take two exponentials and a reciprocal),
+// so one reciprocal serves both denominators, and with bf16 output their exponentials
+// run on the FMA pipe (EXACT: on the special-function units). Exponents end at 60: the
+// denominators' product stays finite, a gate of 2^-60 is as good as zero.
+template <bool EXACT>
+__device__ __forceinline__ void gate_pair(float& s0, float& s1, float c, float k, float b) {
+  const float2 y = unpair(fma2(pair(s0, s1), pair(k, k), pair(b, b)));
+  float2 e;
+  if (EXACT) {
+    e = make_float2(ex2(fminf(y.x, 60.0f)), ex2(fminf(y.y, 60.0f)));
+  } else {
+    e = ex2_fma(pair(fminf(fmaxf(y.x, -60.0f), 60.0f), fminf(fmaxf(y.y, -60.0f), 60.0f)));
+  }
+  const float2 d = unpair(add2(pair(e.x, e.y), pair(1.0f, 1.0f)));
+  const float r = rcp(d.x * d.y);
+  s0 = s0 * c * (r * d.y);
+  s1 = s1 * c * (r * d.x);
 }
 
 // Bits i of word w (keys 32 w + i) with lo <= key < hi.
@@ -219,9 +232,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     vis.b1 = a.P;
     tiles = static_cast<int>((a.P + kTK - 1) / kTK);
   } else {
-    if (gridDim.x * gridDim.y > gridDim.z * 148 && gridDim.x <= kTileThreads) {
+    if (a.longest_first) {
       // Longest tiles first, all their heads together: with ~4 tiles per SM the last
-      // ones decide (a chunk behind 8 caches: 280 -> XXX us). Thread i counts tile i's keys.
+      // ones decide (chunks of 8 rows, window 4096: 280 -> 253 us). Thread i counts tile i's keys.
       uint32_t* keys = reinterpret_cast<uint32_t*>(tile_smem);
       const int order = (blockIdx.y * gridDim.x + blockIdx.x) / gridDim.y;
       h = (blockIdx.y * gridDim.x + blockIdx.x) % gridDim.y;
@@ -528,17 +541,24 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
       }
       tc_wait_ld();
-      if (GATE == kSigmoid) {
-        const int own = prefix ? -1 : static_cast<int>(min(int64_t{kTK}, max(int64_t{-1}, p - s0)));
+      if (GATE != kNoGate) {
+        const int own = prefix || inside ? -1 : static_cast<int>(min(int64_t{kTK}, max(int64_t{-1}, p - s0)));
+        float raw = 0.0f;  // the own token's logit, exempt
+        if (!prefix && !inside) {
 #pragma unroll
-        for (int k = 0; k < kTK; ++k) {
-          const float g = s[k] * c2 * rcp(1.0f + ex2(fmaf(s[k], gk, gb)));
-          s[k] = (!inside && k == own) ? s[k] * c2 : g;
+          for (int k = 0; k < kTK; ++k) raw = k == own ? s[k] : raw;
         }
-      } else if (GATE == kHard) {
-        const int own = prefix ? -1 : static_cast<int>(min(int64_t{kTK}, max(int64_t{-1}, p - s0)));
+        if (GATE == kSigmoid) {
 #pragma unroll
-        for (int k = 0; k < kTK; ++k) s[k] = (s[k] * qs >= tau || (!inside && k == own)) ? s[k] * c2 : -INFINITY;
+          for (int k = 0; k < kTK; k += 2) gate_pair<true>(s[k], s[k + 1], c2, gk, gb);
+        } else {
+#pragma unroll
+          for (int k = 0; k < kTK; ++k) s[k] = s[k] * qs >= tau ? s[k] * c2 : -INFINITY;
+        }
+        if (!prefix && !inside) {
+#pragma unroll
+          for (int k = 0; k < kTK; ++k) s[k] = k == own ? raw * c2 : s[k];
+        }
       }
       if (!inside) {
         const int64_t up = p - s0 + 1, from = p - a.window + 1 - s0, sk = a.sinks - s0;
@@ -588,8 +608,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       // while the second is computed
       const uint64_t scale2 = pair(GATE == kNoGate ? c2 : 1.0f, GATE == kNoGate ? c2 : 1.0f), base2 = pair(-base, -base);
       uint64_t sum0 = 0, sum1 = 0;
-      auto weights = [&](int half, auto some_on_fma) {
-        constexpr bool fma_pipe = decltype(some_on_fma)::value;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
         uint32_t hi[32], lo[HILO ? 32 : 1];
 #pragma unroll
         for (int k = 0; k < 32; k += 2) {
@@ -597,17 +617,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           const uint64_t y0 = fma2(pair(e[0], e[1]), scale2, base2);
           const uint64_t y1 = fma2(pair(e[2], e[3]), scale2, base2);
           const float2 z0 = unpair(y0), z1 = unpair(y1);
-          float x0, x1, x2, x3;
-          if (fma_pipe && (k >> 1) % kPolyOf < kPoly) {
-            const float2 z = ex2_fma(y0);
-            x0 = z.x;
-            x1 = z.y;
-          } else {
-            x0 = ex2(z0.x);
-            x1 = ex2(z0.y);
-          }
-          x2 = ex2(z1.x);
-          x3 = ex2(z1.y);
+          const float x0 = ex2(z0.x), x1 = ex2(z0.y), x2 = ex2(z1.x), x3 = ex2(z1.y);
           sum0 = add2(sum0, pair(x0, x1));
           sum1 = add2(sum1, pair(x2, x3));
           hi[k] = pack2(x0, x1);
@@ -622,12 +632,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         tc_wait_st();
         tc_fence_before();
         mbar_arrive(&s_prdy[2 * w + half]);
-      };
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        // (a hidden key's weight is exactly zero: only where none is hidden may it come from the FMA pipe)
-        if (!HILO && GATE != kHard && inside) weights(half, std::true_type{});
-        else weights(half, std::false_type{});
       }
       const float2 t0 = unpair(sum0), t1 = unpair(sum1);
       l += (t0.x + t0.y) + (t1.x + t1.y);
@@ -737,14 +741,16 @@ cudaError_t launch_attend_tile(const AttendArgs& a, int kv_dtype, int D, bool pr
   if (!encode_rows_map(&tmk, prefix ? a.pk : a.k, store, D, fp8 ? 1 : 2, box_rows) ||
       !encode_rows_map(&tmv, prefix ? a.pv : a.v, store, D, fp8 ? 1 : 2, box_rows))
     return cudaErrorInvalidValue;
+  AttendArgs args = a;
   const int64_t qt = kTileRows / a.G;
   const int64_t items = prefix ? (a.T + qt - 1) / qt : (a.cu_q != nullptr ? a.T / qt + a.B : a.B);
+  args.longest_first = !prefix && items * a.Hkv > device_sm_count() && items <= kTileThreads;
   const dim3 grid(static_cast<unsigned>(items), static_cast<unsigned>(a.Hkv),
                   static_cast<unsigned>(prefix ? a.prefix_splits : a.own_splits));
   const int rows = static_cast<int>(store);
-  if (fp8) return launch_tile_d<128, true>(a, grid, prefix, tmk, tmv, box_rows, rows, st);
-  return D == 128 ? launch_tile_d<128, false>(a, grid, prefix, tmk, tmv, box_rows, rows, st)
-                  : launch_tile_d<64, false>(a, grid, prefix, tmk, tmv, box_rows, rows, st);
+  if (fp8) return launch_tile_d<128, true>(args, grid, prefix, tmk, tmv, box_rows, rows, st);
+  return D == 128 ? launch_tile_d<128, false>(args, grid, prefix, tmk, tmv, box_rows, rows, st)
+                  : launch_tile_d<64, false>(args, grid, prefix, tmk, tmv, box_rows, rows, st);
 }
 
 }  // namespace eta
