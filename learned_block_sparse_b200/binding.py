@@ -444,6 +444,7 @@ class Rope:
 
 
 _NO_ROPE = RopeArgs(None, 0, 0)
+_NO_META = Meta()
 
 
 class Prefix:
@@ -600,30 +601,32 @@ class EtaDecoder:
         if pages is not None and self.sub_blocks > 1:
             raise EtaError(ETA_ERR_UNSUPPORTED, "eta_append_kv")
         _, Hq, Hkv, d, _, _ = self._geometry
-        n = k_new.shape[0]
-        strides = []
-        for x, heads in ((k_new, Hkv), (v_new, Hkv), (q, Hq)):
-            if x is None:
-                strides.append(0)
-                continue
-            at = x.stride()
-            if x.dtype is not self.q_dtype or x.shape != (n, heads, d) or x.get_device() != dev or at[2] != 1 or \
-                    (heads > 1 and at[1] != d):
-                raise ValueError(f"append: new tokens are {self.q_dtype} [n][heads][d] beside K, heads contiguous")
-            strides.append(at[0] if n > 1 else heads * d)  # (a single token's stride means nothing)
+        qt, shape = self.q_dtype, k_new.shape
+        n = shape[0]
+        ks, vs = k_new.stride(), v_new.stride()
+        if k_new.dtype is not qt or v_new.dtype is not qt or shape != (n, Hkv, d) or v_new.shape != shape or \
+                k_new.get_device() != dev or v_new.get_device() != dev or \
+                ks[2] != 1 or vs[2] != 1 or (Hkv > 1 and (ks[1] != d or vs[1] != d)):
+            raise ValueError(f"append: k_new, v_new are {qt} [n][Hkv][d] beside K, heads contiguous")
         q_ptr = out_ptr = None
+        q_stride = 0
         if q is not None:
+            qs, shape = q.stride(), q.shape
+            if q.dtype is not qt or shape != (n, Hq, d) or q.get_device() != dev or qs[2] != 1 or \
+                    (Hq > 1 and qs[1] != d):
+                raise ValueError(f"append: q is {qt} [n][Hq][d] beside K, heads contiguous")
             if q_out is None:
-                q_out = torch.empty((n, Hq, d), dtype=self.q_dtype, device=k.device)
-            elif q_out.dtype is not self.q_dtype or q_out.shape != q.shape or not q_out.is_contiguous() or \
+                q_out = torch.empty((n, Hq, d), dtype=qt, device=k.device)
+            elif q_out.dtype is not qt or q_out.shape != shape or not q_out.is_contiguous() or \
                     q_out.get_device() != dev:
                 raise ValueError("append: q_out is contiguous, of q's shape, type and device")
-            q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
+            q_ptr, out_ptr, q_stride = q.data_ptr(), q_out.data_ptr(), qs[0] if n > 1 else Hq * d
         elif q_out is not None:
             raise ValueError("append: q_out without q")
-        tokens = Tokens(q_ptr, k_new.data_ptr(), v_new.data_ptr(), out_ptr, strides[2], strides[0], strides[1],
-                        None if cu_new is None else cu_new.data_ptr(), n)
-        meta = Meta(self.mu.data_ptr(), self.var.data_ptr(), self.maxnorm.data_ptr()) if build_meta else Meta()
+        # (a single token's stride means nothing)
+        tokens = Tokens(q_ptr, k_new.data_ptr(), v_new.data_ptr(), out_ptr, q_stride, ks[0] if n > 1 else Hkv * d,
+                        vs[0] if n > 1 else Hkv * d, None if cu_new is None else cu_new.data_ptr(), n)
+        meta = Meta(self.mu.data_ptr(), self.var.data_ptr(), self.maxnorm.data_ptr()) if build_meta else _NO_META
         status = lib.eta_append_kv(self._refs[1], ctypes.byref(tokens),
                                    ctypes.byref(_NO_ROPE if rope is None else rope.args), k.data_ptr(), v.data_ptr(),
                                    pages, None if seq_lens is None else seq_lens.data_ptr(), n_tokens, meta,
@@ -652,8 +655,9 @@ class EtaDecoder:
 
     def _query_args(self, q, tau, tau_batch_stride, cu_q, out, dev, what):
         _, Hq, _, d, _, _ = self._geometry
-        n = q.shape[0]
-        if q.dtype is not self.q_dtype or q.shape != (n, Hq, d) or not q.is_contiguous() or q.get_device() != dev:
+        shape = q.shape
+        n = shape[0]
+        if q.dtype is not self.q_dtype or shape != (n, Hq, d) or not q.is_contiguous() or q.get_device() != dev:
             raise ValueError(f"{what}: q is contiguous {self.q_dtype} [n][Hq][d] beside K")
         if out is None:
             if cu_q is not None:
@@ -665,7 +669,7 @@ class EtaDecoder:
             code = ETA_BF16
         else:
             raise TypeError(f"{what}: out is fp32 or bf16")
-        if out.shape != q.shape or not out.is_contiguous() or out.get_device() != dev:
+        if out.shape != shape or not out.is_contiguous() or out.get_device() != dev:
             raise ValueError(f"{what}: out is contiguous, of q's shape, beside K")
         tau_ptr, stride = None, 0
         if tau is not None:
@@ -677,7 +681,7 @@ class EtaDecoder:
                 raise ValueError(f"{what}: tau_batch_stride is 0 or Hq, within tau")
             tau_ptr = tau.data_ptr()
         return ctypes.byref(Queries(q.data_ptr(), None if cu_q is None else cu_q.data_ptr(), n, tau_ptr, stride,
-                                    out.data_ptr(), code)), out
+                                    out.data_ptr(), code)), out, n
 
     def window(self, q, k, v, n_tokens: int, window: int, sinks: int = 0, seq_lens: Optional[torch.Tensor] = None,
                cu_q: Optional[torch.Tensor] = None, tau: Optional[torch.Tensor] = None,
@@ -693,8 +697,9 @@ class EtaDecoder:
             with torch.cuda.device(dev):
                 return self.window(q, k, v, n_tokens, window, sinks, seq_lens, cu_q, tau, tau_batch_stride, out,
                                    block_table, num_pages)
-        queries, out = self._query_args(q, tau, tau_batch_stride, cu_q, out, dev, "window")
-        self.reserve_queries(q.shape[0])
+        queries, out, n = self._query_args(q, tau, tau_batch_stride, cu_q, out, dev, "window")
+        if n > self._reserved:
+            self.reserve_queries(n)
         status = lib.eta_attend_window(self._refs[0], self._refs[2], queries, k.data_ptr(), v.data_ptr(), pages,
                                        None if seq_lens is None else seq_lens.data_ptr(), n_tokens, window, sinks,
                                        self.attend_ws.data_ptr(), self.attend_ws.numel(), _raw_stream(dev))
@@ -714,18 +719,20 @@ class EtaDecoder:
             with torch.cuda.device(dev):
                 return self.shared(q, k, v, n_tokens, prefix, seq_lens, cu_q, tau, tau_batch_stride, out, block_table,
                                    num_pages)
-        queries, out = self._query_args(q, tau, tau_batch_stride, cu_q, out, dev, "shared")
+        queries, out, n = self._query_args(q, tau, tau_batch_stride, cu_q, out, dev, "shared")
         _, _, Hkv, d, bs, _ = self._geometry
         if prefix.n_tokens > 0:
             if (prefix.blocks is None) != (pages is None):
                 raise ValueError("shared: the prefix lies in the pools exactly when the rows do")
-            if prefix.k is not None and (prefix.k.dtype is not self.kv_dtype or prefix.k.get_device() != dev or
-                                         (prefix.k.shape[0], prefix.k.shape[2]) != (Hkv, d)):
-                raise ValueError(f"shared: prefix k, v are {self.kv_dtype} [Hkv][capacity][d] beside K")
-            if prefix.blocks is not None and (prefix.blocks.get_device() != dev or
-                                              prefix.blocks.numel() < -(-prefix.n_tokens // bs)):
+            if pages is None:
+                pk = prefix.k
+                shape = pk.shape
+                if pk.dtype is not self.kv_dtype or pk.get_device() != dev or shape[0] != Hkv or shape[2] != d:
+                    raise ValueError(f"shared: prefix k, v are {self.kv_dtype} [Hkv][capacity][d] beside K")
+            elif prefix.blocks.get_device() != dev or prefix.blocks.numel() * bs < prefix.n_tokens:
                 raise ValueError("shared: prefix blocks cover n_tokens, beside K")
-        self.reserve_queries(q.shape[0])
+        if n > self._reserved:
+            self.reserve_queries(n)
         status = lib.eta_attend_shared(self._refs[0], self._refs[2], queries, ctypes.byref(prefix.args), k.data_ptr(),
                                        v.data_ptr(), pages, None if seq_lens is None else seq_lens.data_ptr(),
                                        n_tokens, self.attend_ws.data_ptr(), self.attend_ws.numel(), _raw_stream(dev))
