@@ -9,7 +9,7 @@
 //                   registers, running max and sum in fp32, weights back to TMEM
 //   warp 8          issues the MMAs: S = Q K^T (128 x 128 x D), O += P V
 //   warp 9          TMA loads of K and V tiles into a ring of buffers
-//   warps 10, 11    fp8 caches: widen the tiles to bf16; else nothing
+//   warps 10 ..     fp8 caches: six warps widen the tiles to bf16; else two idle
 // (warps 8-11 give registers away: of the 168 a thread starts with, the softmax threads
 // end with 208 and hold a whole row)
 // TMEM (512 columns): S0, S1 (128 each; P overwrites S), O0, O1 (D each). The
@@ -32,7 +32,7 @@
 // cycles of the special-function units); long prefixes with few rows are bound by
 // HBM.
 //
-// fp8 (e4m3) caches: the tiles arrive as bytes and warps 10 and 11 widen them to bf16,
+// fp8 (e4m3) caches: the tiles arrive as bytes and six warps widen them to bf16,
 // exactly, into the ring the MMAs read. (f16 would take a third of the conversions, but
 // its weights end at 2^-24 of the largest, and a value that is zero where the largest
 // weight stands then shows the loss.)
@@ -47,7 +47,9 @@ namespace eta {
 
 namespace {
 
-constexpr int kTileThreads = 384;
+constexpr int kTileThreads = 384;     // bf16 caches
+constexpr int kTileThreadsFp8 = 512;  // fp8 caches: a warpgroup more
+constexpr int kConvWarps = 6;         // of them widening
 constexpr int kTR = 128;  // rows per query tile
 constexpr int kTK = 128;  // keys per key tile
 constexpr int kHK = 64;   // keys per half of it: a step of the softmax
@@ -112,41 +114,23 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
   return r;
 }
 
-// 2^x of a pair, |x| <= 126, on the FMA pipe: x = n + f with n the nearest integer (the
-// addition of 1.5 x 2^23 leaves it in the low mantissa bits), 2^f on |f| <= 1/2 by the
-// quartic of least relative error (2.7e-6, fitted by weighted least squares), n added
-// to the exponent.
-__device__ __forceinline__ float2 ex2_fma(uint64_t x) {
-  const uint64_t t = add2(x, pair(12582912.0f, 12582912.0f));
-  const uint64_t n = add2(t, pair(-12582912.0f, -12582912.0f));
-  const uint64_t f = fma2(n, pair(-1.0f, -1.0f), x);
-  uint64_t p = fma2(f, pair(0.0095701022f, 0.0095701022f), pair(0.0559178591f, 0.0559178591f));
-  p = fma2(p, f, pair(0.2402474433f, 0.2402474433f));
-  p = fma2(p, f, pair(0.6931217909f, 0.6931217909f));
-  p = fma2(p, f, pair(0.9999992847f, 0.9999992847f));
-  const float2 u = unpair(t), v = unpair(p);
-  return make_float2(__int_as_float(__float_as_int(v.x) + (__float_as_int(u.x) << 23)),
-                     __int_as_float(__float_as_int(v.y) + (__float_as_int(u.y) << 23)));
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
-// The gate of two logits, in log2 units: s c / (1 + 2^(s k + b)). The special-function
-// units bound a gated tile (each logit would take two exponentials and a reciprocal),
-// so one reciprocal serves both denominators, and with bf16 output their exponentials
-// run on the FMA pipe (EXACT: on the special-function units). Exponents end at 60: the
-// denominators' product stays finite, a gate of 2^-60 is as good as zero.
-template <bool EXACT>
-__device__ __forceinline__ void gate_pair(float& s0, float& s1, float c, float k, float b) {
-  const float2 y = unpair(fma2(pair(s0, s1), pair(k, k), pair(b, b)));
-  float2 e;
-  if (EXACT) {
-    e = make_float2(ex2(fminf(y.x, 60.0f)), ex2(fminf(y.y, 60.0f)));
-  } else {
-    e = ex2_fma(pair(fminf(fmaxf(y.x, -60.0f), 60.0f), fminf(fmaxf(y.y, -60.0f), 60.0f)));
-  }
-  const float2 d = unpair(add2(pair(e.x, e.y), pair(1.0f, 1.0f)));
-  const float r = rcp(d.x * d.y);
-  s0 = s0 * c * (r * d.y);
-  s1 = s1 * c * (r * d.x);
+// The gate of two logits, in log2 units: s c / (1 + 2^(s k + b)). (One reciprocal for
+// both denominators, or their exponentials as polynomials on the FMA pipe, unload the
+// special-function units but cost more instructions: 161 and 183 us where this takes
+// 148, 32 rows behind a 128K prefix, d = 64.)
+__device__ __forceinline__ void gate_pair(float& s0, float& s1, uint64_t c, uint64_t k, uint64_t b) {
+  const uint64_t s = pair(s0, s1);
+  const float2 y = unpair(fma2(s, k, b));
+  const float2 d = unpair(add2(pair(ex2(y.x), ex2(y.y)), pair(1.0f, 1.0f)));
+  const float2 g = unpair(mul2(mul2(s, c), pair(rcp(d.x), rcp(d.y))));
+  s0 = g.x;
+  s1 = g.y;
 }
 
 // Bits i of word w (keys 32 w + i) with lo <= key < hi.
@@ -168,7 +152,7 @@ struct TileSmem {
 };
 
 template <int D, int GATE, bool HILO, bool FP8>
-__global__ void __launch_bounds__(kTileThreads, 1)
+__global__ void __launch_bounds__(FP8 ? kTileThreadsFp8 : kTileThreads, 1)
     attend_tile_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap tmk,
                        const __grid_constant__ CUtensorMap tmv, const int prefix, const int box_rows,
                        const int store_rows) {
@@ -199,12 +183,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (tid == 0) {
     *s_abort = 0;
     for (int i = 0; i < NB; ++i) {
-      mbar_init(&s_full[i], FP8 ? 2 : 1);  // one arrival per converting warp
+      mbar_init(&s_full[i], FP8 ? kConvWarps : 1);  // one arrival per converting warp
       mbar_init(&s_empty[i], 1);
     }
     for (int i = 0; FP8 && i < NR; ++i) {
       mbar_init(&s_rfull[i], 1);
-      mbar_init(&s_rempty[i], 2);
+      mbar_init(&s_rempty[i], kConvWarps);
     }
     for (int w = 0; w < 2; ++w) mbar_init(&s_sfull[w], 2);
     for (int i = 0; i < 4; ++i) mbar_init(&s_prdy[i], 128);
@@ -296,9 +280,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   volatile int* abort_flag = s_abort;
   int armed = 0;  // uses of the ring whose copies were issued (warp 9)
 
-  // 128 x 88 + 256 x 208 registers: the 384 x 168 of the launch
+  // 128 x 88 + 256 x 208 registers: the 384 x 168 of the launch; with fp8 caches
+  // 256 x 48 + 256 x 208: the 512 x 128
   if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 9) {
       // -------------------------------------------------------------- TMA loads
       for (int j = 0; j < n; ++j) {
@@ -429,9 +415,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         __syncwarp();
       }
     } else if (FP8) {
-      // ------------------------------------- fp8 tiles to bf16 (warps 10, 11)
-      // A thread widens 16-byte pieces (16 keys or values of one row) of every second
-      // group of 32; V rows that no query may see become zeros here.
+      // ------------------------------------- fp8 tiles to bf16 (warps 10 .. 15)
+      // A warp widens 16-byte pieces of 32 rows, every sixth group of them; V rows that no
+      // query may see become zeros here. (Two warps: 51 us where six take 45, four
+      // tokens of 16 rows behind an 8K prefix.)
       bool ok = true;
       for (int use = 0; ok && use < 2 * n; ++use) {
         const int raw = use % NR, buf = use % NB, round = use / NB;
@@ -445,10 +432,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const uint32_t groups = paged ? s_pages[(use >> 1) & 7] : 0xffu;
         const unsigned char* src = s_raw + static_cast<size_t>(raw) * kCopy;
         unsigned char* dst = s_kv + static_cast<size_t>(buf) * L::kTile;
-#pragma unroll 4
-        for (int i = 0; i < kTK * 8 / 64; ++i) {
-          const int at = (warp & 1) * 32 + i * 64;           // 32 pieces: rows of one column of pieces
-          const int r = (at & 127) + lane, c = at >> 7;
+#pragma unroll 2
+        for (int g = warp - 10; g < kTK * 8 / 32; g += kConvWarps) {
+          const int r = (g & 3) * 32 + lane, c = g >> 2;
           const uint4 x = *reinterpret_cast<const uint4*>(src + tile_offset(kTK, r, c));
           uint4 lo, hi;
           e4m3_to_bf16(x.x, lo.x, lo.y);
@@ -550,7 +536,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         if (GATE == kSigmoid) {
 #pragma unroll
-          for (int k = 0; k < kTK; k += 2) gate_pair<true>(s[k], s[k + 1], c2, gk, gb);
+          for (int k = 0; k < kTK; k += 2) gate_pair(s[k], s[k + 1], pair(c2, c2), pair(gk, gk), pair(gb, gb));
         } else {
 #pragma unroll
           for (int k = 0; k < kTK; ++k) s[k] = s[k] * qs >= tau ? s[k] * c2 : -INFINITY;
@@ -707,7 +693,7 @@ cudaError_t launch_tile_t(const AttendArgs& a, dim3 grid, bool prefix, const CUt
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(kTileThreads);
+  cfg.blockDim = dim3(FP8 ? kTileThreadsFp8 : kTileThreads);
   cfg.dynamicSmemBytes = TileSmem<D, FP8>::kBytes;
   cfg.stream = st;
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
@@ -744,7 +730,7 @@ cudaError_t launch_attend_tile(const AttendArgs& a, int kv_dtype, int D, bool pr
   AttendArgs args = a;
   const int64_t qt = kTileRows / a.G;
   const int64_t items = prefix ? (a.T + qt - 1) / qt : (a.cu_q != nullptr ? a.T / qt + a.B : a.B);
-  args.longest_first = !prefix && items * a.Hkv > device_sm_count() && items <= kTileThreads;
+  args.longest_first = !prefix && items * a.Hkv > device_sm_count() && items <= (fp8 ? kTileThreadsFp8 : kTileThreads);
   const dim3 grid(static_cast<unsigned>(items), static_cast<unsigned>(a.Hkv),
                   static_cast<unsigned>(prefix ? a.prefix_splits : a.own_splits));
   const int rows = static_cast<int>(store);
