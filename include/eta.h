@@ -447,8 +447,9 @@ ETA_API eta_status_t eta_decode_sparse_static(const eta_shape_t* shape, const et
  *  - Device-side values are checked on the device: a row whose cu range is not
  *    inside [0, n_new] or whose length is below n_b or above n_tokens is skipped
  *    (nothing of it is read, its outputs stay as they were) and
- *    ETA_ERR_INVALID_ARG is recorded in the status word. With cu == NULL a row of
- *    length 0 is idle: skipped without an error.
+ *    ETA_ERR_INVALID_ARG is recorded in the status word. A row without new tokens
+ *    is not looked at; with cu == NULL a row of length 0 is idle, skipped without
+ *    an error.
  *  - pages may be NULL (contiguous cache). A page index outside the pool is never
  *    read or written: ETA_ERR_INVALID_ARG is recorded and what that page would
  *    hold takes no part.

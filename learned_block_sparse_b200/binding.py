@@ -434,7 +434,8 @@ def read_device_status(ws: torch.Tensor, stream=None) -> int:
 class Rope:
     """Rotary positions for :meth:`EtaDecoder.append`: coordinate pair i of the first
     ``2 * len(inv_freq)`` coordinates turns by position * inv_freq[i] (fp32, on the
-    device). Pairs are (i, i + rot_dim / 2), or neighbours with ``interleaved``."""
+    device). Pairs are (i, i + rot_dim / 2), or neighbours with ``interleaved``. A model
+    keeps one and passes it to every call."""
 
     def __init__(self, inv_freq: torch.Tensor, interleaved: bool = False):
         if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
@@ -600,6 +601,8 @@ class EtaDecoder:
                                    num_pages, build_meta)
         if pages is not None and self.sub_blocks > 1:
             raise EtaError(ETA_ERR_UNSUPPORTED, "eta_append_kv")
+        if rope is not None and rope.inv_freq.get_device() != dev:
+            raise ValueError("append: the rope's inv_freq is not beside K")
         _, Hq, Hkv, d, _, _ = self._geometry
         qt, shape = self.q_dtype, k_new.shape
         n = shape[0]

@@ -110,7 +110,7 @@ def reference(p, window=None, sinks=0, gated=False, hard=False, prefix=False):
     dev = p["q"].device
     out = torch.full((T, c.Hq, c.d), float("nan"), dtype=torch.float64, device=dev)
     mass = torch.zeros_like(out)                                            # sum of weight x |v|
-    info = torch.zeros((T, c.Hq, 4), dtype=torch.float64, device=dev)       # |q||k| sums, |g|, keys, gate gain
+    info = torch.zeros((T, c.Hq, 4), dtype=torch.float64, device=dev)       # |q||k| sums, |g|, keys, largest |v|
     P = p["prefix_len"] if prefix else 0
     for b, (n, length) in enumerate(c.rows):
         n = n if c.packed else (1 if length else 0)
@@ -151,21 +151,23 @@ def reference(p, window=None, sinks=0, gated=False, hard=False, prefix=False):
         info[t0: t0 + n, :, 0] = (gain * scale).masked_fill(dead, 0).amax(-1).T
         info[t0: t0 + n, :, 1] = g.abs().masked_fill(dead, 0).amax(-1).T
         info[t0: t0 + n, :, 2] = seen.sum(-1).double()[:, None]
+        info[t0: t0 + n, :, 3] = vh.abs().nan_to_num(0.0).amax((-1, -2))
     return out, mass, info
 
 
-def bound(out, mass, info, out_dtype):
+def bound(out, mass, info, out_dtype, floor=0.0):
     """How far a result may be from the 64-bit one. A weight's relative error is the
     error of its logit (d products and additions of 2^-22 each, fp8 queries held to
     2^-21 of their largest; times the gate's slope), plus its own evaluation (2^-22,
     and 2^-23 of the exponent for its rounding), and enters the numerator and the
-    denominator: twice. Sums over N keys add N 2^-23. Weights that meet values as
+    denominator: twice. `floor`: what a weight may lose however small it is (of the
+    largest weight, which is at most the sum), times the N keys' largest value. Sums over N keys add N 2^-23. Weights that meet values as
     bf16 numbers are off by 2^-8 each (bf16 output), as two bf16 numbers by 2^-16
     (fp32 output). Every error is weighted by sum w |v|. Then the output's rounding."""
     rel = 2 * (info[..., 0] + 2.0 ** -22 + 2.0 ** -23 * info[..., 1]) + 2.0 ** -23 * info[..., 2]
     rel = rel + (2.0 ** -8 if out_dtype == torch.bfloat16 else 2.0 ** -16)
     last = 2.0 ** -8 if out_dtype == torch.bfloat16 else 2.0 ** -24
-    tol = rel[..., None] * mass
+    tol = rel[..., None] * mass + floor * info[..., 2, None] * info[..., 3, None]
     return tol + last * (out.abs() + tol)
 
 
@@ -181,14 +183,14 @@ def live_tokens(c: Case):
     return live
 
 
-def check(p, got, ref, fill):
+def check(p, got, ref, fill, floor=0.0):
     """Live tokens within the bound, every other output as it was (`fill`)."""
     out, mass, info = ref
     live = live_tokens(p["case"]).to(got.device)
     x = got.float().double()
     assert torch.equal(got[~live], torch.full_like(got[~live], fill))
     err = (x - out).abs()[live]
-    tol = bound(out, mass, info, got.dtype)[live]
+    tol = bound(out, mass, info, got.dtype, floor)[live]
     assert torch.isfinite(x[live]).all()
     # an output that is exactly zero (one visible key, a zero value) has no room at all
     worst = torch.where(err == 0, torch.zeros_like(err), err / tol).max().item() if err.numel() else 0.0

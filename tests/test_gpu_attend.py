@@ -299,3 +299,136 @@ def test_a_prompt_and_its_decode_steps_together(kv):
     for a, b in zip(dec.meta, built.meta):
         for row, nfull in enumerate(full):
             assert torch.equal(a[row, ..., :nfull], b[row, ..., :nfull])
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "f32"])
+def test_peaked_and_flat_logits_of_single_tokens(kv):
+    """As above for one token per row. With fp8 values a weight is two f16 numbers, which
+    end at 2^-24 of the largest weight: it may lose half of that."""
+    c = Case(kv=kv, q="f32" if kv == "f32" else "bf16", rows=((1, 400), (1, 256), (1, 33)), seed=8)
+    for scale in (40.0, 0.0):
+        p, whole = make(c, prefix=300), make(c, prefix=300)
+        p["q"].mul_(scale), whole["q"].mul_(scale)
+        floor = 2.0 ** -25 if kv == "fp8" else 0.0
+        check(p, run_window(p, 128, 4, out="f32"), reference(p, 128, 4), FILL, floor)
+        check(whole, run_shared(whole, out="f32"), reference(whole, prefix=True), FILL, floor)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_pages_past_32_bit_offsets(packed):
+    """A pool of 2.3e9 elements: rows in its last pages give the bits they give in a small one."""
+    rows = ((40, 300), (3, 65), (100, 128)) if packed else ((1, 300), (1, 65), (1, 128))
+    c = Case(Hq=8, Hkv=8, bs=32, cap=320, paged=True, rows=rows, packed=packed, seed=2)
+    p = make(c, prefix=90)
+    pages, small = 70000, p["K"].shape[0]
+    far = dict(p)
+    for name in ("K", "V"):
+        far[name] = torch.empty((pages, c.Hkv, c.bs, c.d), dtype=torch.bfloat16, device="cuda")
+        far[name][pages - small:] = p[name]
+    far["table"] = p["table"] + (pages - small)
+    far["blocks"] = p["blocks"] + (pages - small)
+    far["page_args"] = dict(block_table=far["table"], num_pages=pages)
+    far["prefix"] = binding.Prefix(90, blocks=far["blocks"])
+    g = torch.Generator().manual_seed(4)
+    new = [torch.randn((c.T, h, c.d), generator=g).to(torch.bfloat16).cuda() for h in (c.Hkv, c.Hkv)]
+    got = []
+    for r in (p, far):
+        dec = decoder(c)
+        dec.append(*new, r["K"], r["V"], c.cap, seq_lens=r["lens"], cu_new=r["cu"], **r["page_args"])
+        got.append((run_window(r, 50, 4, dec=dec, hide=False), run_shared(r, dec=dec), dec.mu, dec.var, dec.maxnorm,
+                    r["K"][pages - small:] if r is far else r["K"], r["V"][pages - small:] if r is far else r["V"]))
+    for a, b in zip(*got):
+        assert torch.equal(a.view(torch.int16 if a.dtype == torch.bfloat16 else torch.int32),
+                           b.view(torch.int16 if b.dtype == torch.bfloat16 else torch.int32))
+
+
+def test_two_calls_at_once_on_two_streams():
+    """Two decoders (workspaces) on two streams give what each gives alone, again and again."""
+    cases = [Case(rows=((1, 500), (1, 90), (1, 512)), seed=1), Case(rows=((70, 300), (5, 512)), packed=True, seed=2)]
+    ps = [make(c, prefix=200) for c in cases]
+    decs = [decoder(c) for c in cases]
+    alone = [(run_window(p, 100, 4, dec=d, hide=False), run_shared(p, dec=d)) for p, d in zip(ps, decs)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = [[torch.empty_like(alone[i][0]) for _ in range(16)] for i in range(2)]
+    torch.cuda.synchronize()
+    for k in range(8):
+        for i, (p, d, s) in enumerate(zip(ps, decs, streams)):
+            c = p["case"]
+            with torch.cuda.stream(s):
+                d.window(p["q"], p["K"], p["V"], c.cap, 100, sinks=4, seq_lens=p["lens"], cu_q=p["cu"],
+                         out=outs[i][2 * k])
+                d.shared(p["q"], p["K"], p["V"], c.cap, p["prefix"], seq_lens=p["lens"], cu_q=p["cu"],
+                         out=outs[i][2 * k + 1])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert decs[i].device_status() == 0
+        for k in range(8):
+            assert torch.equal(outs[i][2 * k], alone[i][0]) and torch.equal(outs[i][2 * k + 1], alone[i][1])
+
+
+def test_a_captured_chunk_follows_offsets_and_lengths():
+    """A captured packed call replayed while the rows' shares of the tokens change, to none and back."""
+    c = Case(rows=((30, 200), (34, 90), (0, 10)), packed=True, seed=5)
+    p = make(c, prefix=64)
+    dec = decoder(c)
+    o = [torch.full((c.T, c.Hq, c.d), FILL, device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+
+    def call():
+        dec.window(p["q"], p["K"], p["V"], c.cap, 77, sinks=2, seq_lens=p["lens"], cu_q=p["cu"], out=o[0])
+        dec.shared(p["q"], p["K"], p["V"], c.cap, p["prefix"], seq_lens=p["lens"], cu_q=p["cu"], out=o[1])
+
+    call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for rows in (((64, 200), (0, 90), (0, 10)), ((0, 200), (1, 90), (10, 10)), ((0, 200), (0, 90), (0, 10)), c.rows):
+        r = dict(p)
+        r["case"] = Case(**{**c.__dict__, "rows": rows, "pad": c.T - sum(n for n, _ in rows)})
+        cu = [0]
+        for n, _ in rows:
+            cu.append(cu[-1] + n)
+        r["cu_list"] = cu
+        p["cu"].copy_(torch.tensor(cu, dtype=torch.int32))
+        for x in o:
+            x.fill_(FILL)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert dec.device_status() == 0
+        check(r, o[0], reference(r, 77, 2), FILL)
+        check(r, o[1], reference(r, prefix=True), FILL)
+
+
+def test_calls_that_cannot_be_right_are_refused():
+    c = Case(rows=((1, 100), (1, 50)), seed=1)
+    p = make(c, prefix=40)
+    dec = decoder(c)
+    K, V, q, lens = p["K"], p["V"], p["q"], p["lens"]
+    good = dict(seq_lens=lens)
+    dec.window(q, K, V, c.cap, 10, **good)
+    one = torch.zeros((2, c.Hkv, c.d), dtype=torch.bfloat16, device="cuda")
+    bad = [
+        lambda: dec.window(q.cpu(), K, V, c.cap, 10), lambda: dec.window(q.float(), K, V, c.cap, 10),
+        lambda: dec.window(q, K.cpu(), V.cpu(), c.cap, 10), lambda: dec.window(q, K[:, :, :64], V[:, :, :64], c.cap, 10),
+        lambda: dec.window(q, K.transpose(1, 2), V.transpose(1, 2), c.cap, 10),
+        lambda: dec.window(q, K, V, c.cap, 10, seq_lens=lens.long()), lambda: dec.window(q, K, V, c.cap, 10, seq_lens=lens[:1]),
+        lambda: dec.window(q, K, V, c.cap, 10, cu_q=p["lens"]), lambda: dec.window(q, K, V, c.cap, 0),
+        lambda: dec.window(q, K, V, c.cap + 1, 10), lambda: dec.window(q, K, V, c.cap, 10, sinks=-1),
+        lambda: dec.window(q, K, V, c.cap, 10, out=torch.empty((2, c.Hq, c.d), dtype=torch.float16, device="cuda")),
+        lambda: dec.window(q, K, V, c.cap, 10, out=torch.empty((1, c.Hq, c.d), device="cuda")),
+        lambda: dec.window(q, K, V, c.cap, 10, tau=p["tau"].double()), lambda: dec.window(q, K, V, c.cap, 10, tau=p["tau"][0], tau_batch_stride=c.Hq),
+        lambda: dec.window(q, K, V, c.cap, 10, block_table=torch.zeros(3, dtype=torch.int32, device="cuda")),
+        lambda: dec.shared(q, K, V, c.cap, binding.Prefix(8, blocks=torch.zeros(1, dtype=torch.int32, device="cuda"))),
+        lambda: dec.shared(q, K, V, c.cap, binding.Prefix(8, k=p["PK"].cpu(), v=p["PV"].cpu())),
+        lambda: dec.shared(q, K, V, c.cap, binding.Prefix(8, k=p["PK"][:1], v=p["PV"][:1])),
+        lambda: dec.append(one, one.float(), K, V, c.cap), lambda: dec.append(one[:1], one[:1], K, V, c.cap),
+        lambda: dec.append(one.transpose(0, 1), one.transpose(0, 1), K, V, c.cap),
+        lambda: dec.append(one, one, K, V, c.cap, q=q[:, :4]), lambda: dec.append(one, one, K, V, c.cap, q_out=q),
+        lambda: dec.append(one, one, K, V, c.cap, rope=binding.Rope(torch.zeros(64))),
+        lambda: dec.append(one, one, K, V, c.cap, rope=binding.Rope(torch.zeros(65, device="cuda"))),
+    ]
+    for i, f in enumerate(bad):
+        with pytest.raises((ValueError, TypeError, binding.EtaError)):
+            f()
+            print("accepted", i)
+    torch.cuda.synchronize()
+    assert dec.device_status() == 0
