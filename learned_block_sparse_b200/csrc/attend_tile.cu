@@ -8,7 +8,7 @@
 //   warps 0-3, 4-7  softmax of tile 0, 1: thread = row, the row's 128 logits in
 //                   registers, running max and sum in fp32, weights back to TMEM
 //   warp 8          issues the MMAs: S = Q K^T (128 x 128 x D), O += P V
-//   warp 9          TMA loads of K and V tiles into a ring of buffers
+//   warp 9          TMA loads: the query tiles, then K and V tiles into a ring of buffers
 //   warps 10 ..     fp8 caches: six warps widen the tiles to bf16; else two idle
 // (warps 8-11 give registers away: of the 168 a thread starts with, the softmax threads
 // end with 208 and hold a whole row)
@@ -153,8 +153,8 @@ struct TileSmem {
 
 template <int D, int GATE, bool HILO, bool FP8>
 __global__ void __launch_bounds__(FP8 ? kTileThreadsFp8 : kTileThreads, 1)
-    attend_tile_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap tmk,
-                       const __grid_constant__ CUtensorMap tmv, const int prefix, const int box_rows,
+    attend_tile_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap tmq,
+                       const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const int prefix, const int box_rows,
                        const int store_rows) {
   using L = TileSmem<D, FP8>;
   constexpr int NB = L::kBufs;                    // the ring the MMAs read
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(FP8 ? kTileThreadsFp8 : kTileThreads, 1)
     }
     for (int w = 0; w < 2; ++w) mbar_init(&s_sfull[w], 2);
     for (int i = 0; i < 4; ++i) mbar_init(&s_prdy[i], 128);
-    mbar_init(s_qrdy, 256);
+    mbar_init(s_qrdy, 1);
     mbar_init(s_ofull, 1);
     fence_mbar_init();
   }
@@ -287,6 +287,16 @@ __global__ void __launch_bounds__(FP8 ? kTileThreadsFp8 : kTileThreads, 1)
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 9) {
       // -------------------------------------------------------------- TMA loads
+      // the queries: rows past the tile's are other tokens or zeros, their results unused
+      if (lane == 0) {
+        mbar_arrive_expect_tx(s_qrdy, ntiles * L::kQ);
+        for (int w = 0; w < ntiles; ++w)
+#pragma unroll
+          for (int x = 0; x < D / 64; ++x)
+            tma_load_box3(s_q + w * L::kQ + x * kTR * 128, &tmq, x * 64, h * G,
+                          static_cast<int>(t.tok0) + (w << (qt_log2 - 1)), s_qrdy);
+      }
+      __syncwarp();
       for (int j = 0; j < n; ++j) {
         int64_t s0;
         int v0, v1;
@@ -465,24 +475,6 @@ __global__ void __launch_bounds__(FP8 ? kTileThreadsFp8 : kTileThreads, 1)
     auto q_row = [&](int r_) {                     // row of q (and of the output) of block row r_
       return (t.tok0 + (r_ >> g_log2)) * a.Hq + h * G + (r_ & (G - 1));
     };
-    {
-      // the tile's queries, D / 8 threads per row (coalesced)
-      constexpr int P = D / 8, RPP = 128 / P;
-      unsigned char* dst = s_q + w * L::kQ;
-      const int c = r % P;
-      uint4 x[P];  // all in flight
-#pragma unroll
-      for (int i = 0; i < P; ++i) {
-        const int rr = i * RPP + r / P;
-        x[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (w * kTR + rr < rows)
-          x[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + q_row(w * kTR + rr) * D) + c);
-      }
-#pragma unroll
-      for (int i = 0; i < P; ++i) *reinterpret_cast<uint4*>(dst + tile_offset(kTR, i * RPP + r / P, c)) = x[i];
-      fence_async_smem();
-      mbar_arrive(s_qrdy);
-    }
     const int64_t p = t.p0 + (row >> g_log2);      // this row's position (prefix: past every key)
     const float qs = a.qscale, c2 = qs * kLog2e;   // logit = S qs, in log2 units S c2
     float tau = 0.0f;
@@ -630,12 +622,11 @@ __global__ void __launch_bounds__(FP8 ? kTileThreadsFp8 : kTileThreads, 1)
       const int64_t part = static_cast<int64_t>(prefix ? a.own_splits + split : split) * a.T * a.Hq;
       const float inv = direct ? (l > 0.0f ? 1.0f / l : 0.0f) : 1.0f;
       if (live && !direct) a.ml_part[part + q_row(row)] = make_float2(m, l);
-      // Through shared memory (query tiles and ring are free), 128 bytes of 32 rows a
-      // slab, so that eight lanes write one row's 128 bytes.
+      // Through shared memory (query tiles and ring are free; rows padded by 16 bytes, so
+      // that eight lanes store to eight bank groups), then one bulk copy per row.
       const bool narrow = direct && a.out_dtype == ETA_BF16;
-      unsigned char* stage = s_q + warp * (D / 32) * 4096;
-      const int row0 = w * kTR + (warp & 3) * 32;
       if (n > 0) {
+        unsigned char* mine = s_q + (w * kTR + r) * (D * 4 + 16);
         float o[D];
 #pragma unroll
         for (int k = 0; k < D / 32; ++k) tmem_ld32(so + 32 * k, reinterpret_cast<uint32_t*>(o) + 32 * k);
@@ -643,27 +634,23 @@ __global__ void __launch_bounds__(FP8 ? kTileThreadsFp8 : kTileThreads, 1)
         if (narrow) {
 #pragma unroll
           for (int e = 0; e < D; e += 8)
-            *reinterpret_cast<uint4*>(stage + (e >> 6) * 4096 + tile_offset(32, lane, (e >> 3) & 7)) =
+            *reinterpret_cast<uint4*>(mine + 2 * e) =
                 make_uint4(pack2(o[e] * inv, o[e + 1] * inv), pack2(o[e + 2] * inv, o[e + 3] * inv),
                            pack2(o[e + 4] * inv, o[e + 5] * inv), pack2(o[e + 6] * inv, o[e + 7] * inv));
         } else {
 #pragma unroll
           for (int e = 0; e < D; e += 4)
-            *reinterpret_cast<float4*>(stage + (e >> 5) * 4096 + tile_offset(32, lane, (e >> 2) & 7)) =
+            *reinterpret_cast<float4*>(mine + 4 * e) =
                 make_float4(o[e] * inv, o[e + 1] * inv, o[e + 2] * inv, o[e + 3] * inv);
         }
-        __syncwarp();
-        unsigned char* out = direct ? static_cast<unsigned char*>(a.out)
-                                    : reinterpret_cast<unsigned char*>(a.o_part + part * D);
-        const int slabs = narrow ? D / 64 : D / 32;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int rr = 4 * k + (lane >> 3), c = lane & 7;
-          if (row0 + rr >= rows) continue;
-          unsigned char* dst = out + q_row(row0 + rr) * (slabs * 128) + 16 * c;
-          for (int q = 0; q < slabs; ++q)
-            *reinterpret_cast<uint4*>(dst + 128 * q) =
-                *reinterpret_cast<const uint4*>(stage + q * 4096 + tile_offset(32, rr, c));
+        fence_async_smem();
+        if (live) {
+          const int bytes = narrow ? D * 2 : D * 4;
+          unsigned char* out = direct ? static_cast<unsigned char*>(a.out)
+                                      : reinterpret_cast<unsigned char*>(a.o_part + part * D);
+          bulk_store(out + q_row(row) * bytes, mine, bytes);
+          bulk_commit();
+          bulk_wait_read();
         }
       }
       tc_fence_before();
@@ -671,7 +658,11 @@ __global__ void __launch_bounds__(FP8 ? kTileThreadsFp8 : kTileThreads, 1)
   }
   __syncthreads();
   if (*abort_flag && warp == 9 && lane == 0) {
-    // an aborted block may have copies in flight: the last use of every buffer lands before it exits
+    // an aborted block may have copies in flight: the queries and the last use of every
+    // buffer land before it exits
+    const uint64_t tq = global_timer_ns();
+    while (!mbar_try_wait(s_qrdy, 0) && global_timer_ns() - tq < kWaitLimitNs) {
+    }
     for (int use = max(0, armed - NR); use < armed; ++use) {
       const uint64_t t0 = global_timer_ns();
       while (!mbar_try_wait(&s_rfull[use % NR], (use / NR) & 1) && global_timer_ns() - t0 < kWaitLimitNs) {
@@ -686,7 +677,8 @@ __global__ void __launch_bounds__(FP8 ? kTileThreadsFp8 : kTileThreads, 1)
 }
 
 template <int D, int GATE, bool HILO, bool FP8>
-cudaError_t launch_tile_t(const AttendArgs& a, dim3 grid, bool prefix, const CUtensorMap& tmk, const CUtensorMap& tmv,
+cudaError_t launch_tile_t(const AttendArgs& a, dim3 grid, bool prefix, const CUtensorMap& tmq, const CUtensorMap& tmk,
+                          const CUtensorMap& tmv,
                           int box_rows, int store_rows, cudaStream_t st) {
   static std::atomic<uint64_t> smem_done{0};
   cudaError_t e = allow_max_smem(smem_done, reinterpret_cast<const void*>(attend_tile_kernel<D, GATE, HILO, FP8>));
@@ -699,18 +691,19 @@ cudaError_t launch_tile_t(const AttendArgs& a, dim3 grid, bool prefix, const CUt
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, attend_tile_kernel<D, GATE, HILO, FP8>, a, tmk, tmv, prefix ? 1 : 0, box_rows, store_rows);
+  e = cudaLaunchKernelEx(&cfg, attend_tile_kernel<D, GATE, HILO, FP8>, a, tmq, tmk, tmv, prefix ? 1 : 0, box_rows, store_rows);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <int D, bool FP8>
-cudaError_t launch_tile_d(const AttendArgs& a, dim3 grid, bool prefix, const CUtensorMap& tmk, const CUtensorMap& tmv,
+cudaError_t launch_tile_d(const AttendArgs& a, dim3 grid, bool prefix, const CUtensorMap& tmq, const CUtensorMap& tmk,
+                          const CUtensorMap& tmv,
                           int box_rows, int store_rows, cudaStream_t st) {
   const int gate = a.tau == nullptr ? kNoGate : (a.gate == ETA_GATE_HARD ? kHard : kSigmoid);
   const bool two = a.out_dtype == ETA_F32;
 #define ETA_TILE(g)                                                                                         \
-  (two ? launch_tile_t<D, g, true, FP8>(a, grid, prefix, tmk, tmv, box_rows, store_rows, st)               \
-       : launch_tile_t<D, g, false, FP8>(a, grid, prefix, tmk, tmv, box_rows, store_rows, st))
+  (two ? launch_tile_t<D, g, true, FP8>(a, grid, prefix, tmq, tmk, tmv, box_rows, store_rows, st)               \
+       : launch_tile_t<D, g, false, FP8>(a, grid, prefix, tmq, tmk, tmv, box_rows, store_rows, st))
   return gate == kNoGate ? ETA_TILE(kNoGate) : (gate == kSigmoid ? ETA_TILE(kSigmoid) : ETA_TILE(kHard));
 #undef ETA_TILE
 }
@@ -723,8 +716,8 @@ cudaError_t launch_attend_tile(const AttendArgs& a, int kv_dtype, int D, bool pr
   const int64_t store = paged ? static_cast<int64_t>(a.num_pages) * a.Hkv * a.bs
                               : (prefix ? a.Hkv * a.pcap : static_cast<int64_t>(a.B) * a.Hkv * a.cap);
   const int box_rows = paged ? a.bs : kTK;
-  CUtensorMap tmk, tmv;
-  if (!encode_rows_map(&tmk, prefix ? a.pk : a.k, store, D, fp8 ? 1 : 2, box_rows) ||
+  CUtensorMap tmq, tmk, tmv;
+  if (!encode_query_map(&tmq, a.q, a.T, a.Hq, a.G, D) || !encode_rows_map(&tmk, prefix ? a.pk : a.k, store, D, fp8 ? 1 : 2, box_rows) ||
       !encode_rows_map(&tmv, prefix ? a.pv : a.v, store, D, fp8 ? 1 : 2, box_rows))
     return cudaErrorInvalidValue;
   AttendArgs args = a;
@@ -734,9 +727,9 @@ cudaError_t launch_attend_tile(const AttendArgs& a, int kv_dtype, int D, bool pr
   const dim3 grid(static_cast<unsigned>(items), static_cast<unsigned>(a.Hkv),
                   static_cast<unsigned>(prefix ? a.prefix_splits : a.own_splits));
   const int rows = static_cast<int>(store);
-  if (fp8) return launch_tile_d<128, true>(args, grid, prefix, tmk, tmv, box_rows, rows, st);
-  return D == 128 ? launch_tile_d<128, false>(args, grid, prefix, tmk, tmv, box_rows, rows, st)
-                  : launch_tile_d<64, false>(args, grid, prefix, tmk, tmv, box_rows, rows, st);
+  if (fp8) return launch_tile_d<128, true>(args, grid, prefix, tmq, tmk, tmv, box_rows, rows, st);
+  return D == 128 ? launch_tile_d<128, false>(args, grid, prefix, tmq, tmk, tmv, box_rows, rows, st)
+                  : launch_tile_d<64, false>(args, grid, prefix, tmq, tmk, tmv, box_rows, rows, st);
 }
 
 }  // namespace eta

@@ -109,6 +109,22 @@ __device__ __forceinline__ void tma_load_rows(void* dst, const CUtensorMap* tm, 
       : "memory");
 }
 
+__device__ __forceinline__ void tma_load_box3(void* dst, const CUtensorMap* tm, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          smem_u32(dst)),
+      "l"(tm), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+// `bytes` (a multiple of 16) from shared to global memory, both 16-byte aligned, in this
+// thread's bulk group; bulk_wait_read: the shared memory of its groups has been read.
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+
 // Byte offset of 16-byte piece `c` of row `row` in a tile kept as 128-byte column
 // boxes of `rows` rows with the 128-byte swizzle.
 __device__ __forceinline__ uint32_t tile_offset(int rows, int row, int c) {
@@ -126,6 +142,20 @@ inline PFN_cuTensorMapEncodeTiled_v12000 attend_map_encoder() {
       fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
   });
   return fn;
+}
+
+// Packed bf16 queries [T][Hq][d] in boxes of 64 coordinates of G heads of 128 / G
+// tokens: a query tile's 128 rows, token by token; tokens past T read as zeros.
+inline bool encode_query_map(CUtensorMap* tm, const void* q, int64_t T, int Hq, int G, int d) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = attend_map_encoder();
+  if (enc == nullptr) return false;
+  const cuuint64_t gdim[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(Hq), static_cast<cuuint64_t>(T)};
+  const cuuint64_t gstride[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(Hq) * d * 2};
+  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(128 / G)};
+  const cuuint32_t estride[3] = {1u, 1u, 1u};
+  return enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), gdim, gstride, box, estride,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // [rows][d] view of a K or V store of eb-byte elements (2: bf16, 1: fp8 bytes) in
