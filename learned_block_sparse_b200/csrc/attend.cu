@@ -69,15 +69,21 @@ int clamp_splits(int64_t s, int64_t most) { return static_cast<int>(s > most ? (
 
 // The pass over `keys` keys of T packed queries (own: in `rows` rows, cu given or
 // one each).
-Pass pass_of(const eta_shape_t& s, int64_t T, bool prefix, bool single, int64_t keys) {
+Pass pass_of(const eta_shape_t& s, int64_t T, int out_dtype, bool prefix, bool single, int64_t keys) {
   const int64_t G = s.n_q_heads / s.n_kv_heads, sms = device_sm_count();
   Pass p;
   const bool mma = s.kv_dtype == ETA_FP8_E4M3 || (s.kv_dtype == ETA_BF16 && s.q_dtype == ETA_BF16);
   p.kernel = !prefix && single ? (mma ? kRow : kStream) : (mma ? kTile : kSimt);
-  const int64_t qt = (p.kernel == kTile ? kTileRows : kSimtRows) / G;
+  const int64_t qt = (p.kernel == kTile ? tile_rows(out_dtype) : kSimtRows) / G;
   const int64_t items = (prefix ? (T + qt - 1) / qt : (single ? s.batch : T / qt + s.batch)) * s.n_kv_heads;
-  if (p.kernel == kTile)       // one thread block per SM, in one wave
-    p.splits = clamp_splits(sms / items, prefix ? keys / 128 : keys / 256);
+  if (p.kernel == kTile) {     // one thread block per SM, in one wave
+    // Blocks of half the rows (fp32 output) may take two waves where that leaves fewer
+    // SMs idle: 96 items are 96 blocks of all keys or 288 of a third each (64 new tokens
+    // in 8 rows, 16 KV heads of 64, behind 32K keys: 864 -> 547 us).
+    const int64_t s1 = sms / items, s2 = 2 * sms / items;
+    const bool two = tile_rows(out_dtype) < kTileRows && 2 * (s1 < 1 ? 1 : s1) < s2;
+    p.splits = clamp_splits(two ? s2 : s1, prefix ? keys / 128 : keys / 256);
+  }
   else if (p.kernel != kSimt)  // three thread blocks per SM, three waves (the last one is rarely full); 64 keys at least
     p.splits = clamp_splits((kRowWant * sms + items - 1) / items, keys / 64);
   else                         // about four thread blocks per SM
@@ -92,7 +98,8 @@ size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Partial rows (splits x query rows) the passes of a call of up to T queries can
 // leave: at most R (want + items) with splits <= want / items + 1 and R rows per
-// item (kSimt; kRow, kStream: R = G), at most R want with splits <= want / items (kTile), never below the
+// item (kSimt; kRow, kStream: R = G), at most R want with splits <= want / items (kTile:
+// 256 rows and one wave, or 128 rows and two), never below the
 // query rows when there are two passes. A single pass that is not split leaves
 // none. Non-decreasing in T.
 size_t attend_workspace_bytes(const eta_shape_t& s, int64_t T, bool with_prefix) {
@@ -110,8 +117,8 @@ cudaError_t launch_attend(const AttendCall& c, cudaStream_t st) {
   AttendArgs a = make_attend_args(c);
   const int D = c.shape.head_dim;
   const int64_t own_keys = a.sinks + a.window < a.n ? a.sinks + a.window : a.n;
-  const Pass own = pass_of(c.shape, a.T, false, a.cu_q == nullptr, own_keys);
-  const Pass pre = pass_of(c.shape, a.T, true, false, a.P);
+  const Pass own = pass_of(c.shape, a.T, a.out_dtype, false, a.cu_q == nullptr, own_keys);
+  const Pass pre = pass_of(c.shape, a.T, a.out_dtype, true, false, a.P);
   a.own_splits = own.splits;
   a.prefix_splits = a.P > 0 ? pre.splits : 0;
   const int slots = a.own_splits + a.prefix_splits;

@@ -14,9 +14,15 @@
 // thread blocks fit per SM (64 KB each): 96 KB in flight, and three warps per
 // scheduler hide each other's dependent chains.
 //
-// Rounding: the weights' fp32 value is split into two bf16 (f16 with fp8 values)
-// numbers, the first in rows 0-7 of the A operand, the remainder in rows 8-15, so one
-// MMA carries 16 bits of every weight.
+// Rounding: a weight is split into two bf16 numbers (with fp8 values two f16 numbers),
+// the first in rows 0-7 of the A operand, the remainder in rows 8-15, so one MMA carries
+// 16 (22) bits of every weight. With fp32 output a second MMA of bf16 values adds what
+// is left, 24 bits in all (1e-6 of the result at 4K keys, 295 us for 64 rows, as without).
+//
+// Measured: 64 rows of fp8, 8 KV heads, window 4,096: 107 us of the kernel (0.71 of the
+// copy bandwidth for the whole call, 111 us); issue-bound (54% issue slots, `wait` the
+// top stall): the widening of fp8 and the softmax of half-empty tiles. The own keys of
+// 64 bf16 rows beside a prefix: 36 us alone, hidden in part behind the prefix.
 //
 // Keys of a chunk that the token does not see (a chunk's ends, a page outside the
 // pool) may hold anything: their logits become -inf and their V rows are zeroed in
@@ -227,6 +233,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowBlocks)
   const bool gated = a.tau != nullptr;
   const float tau = gated && live ? a.tau[t.tok0 * a.tau_stride + h * G + row] : 0.0f;
   const float nbl = -a.beta * kLog2e;
+  const bool fine = a.out_dtype == ETA_F32;
 
   float o[NDT][4];
 #pragma unroll
@@ -372,13 +379,19 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowBlocks)
           return *reinterpret_cast<const uint32_t*>(&v);
         };
         const uint32_t h0 = pack(p0, p1), h1 = pack(p2, p3);
-        const uint32_t l0 = pack(p0 - bf16_lo(h0), p1 - bf16_hi(h0)), l1 = pack(p2 - bf16_lo(h1), p3 - bf16_hi(h1));
+        const float r0 = p0 - bf16_lo(h0), r1 = p1 - bf16_hi(h0), r2 = p2 - bf16_lo(h1), r3 = p3 - bf16_hi(h1);
+        const uint32_t l0 = pack(r0, r1), l1 = pack(r2, r3);
+        const uint32_t e0 = pack(r0 - bf16_lo(l0), r1 - bf16_hi(l0)), e1 = pack(r2 - bf16_lo(l1), r3 - bf16_hi(l1));
 #pragma unroll
         for (int jd = 0; jd < NDT; jd += 2) {
           uint32_t r[4];
           ldm4_t((vt ^ ((jd & 7) << 4)) + (jd >> 3) * CH * 128 + m2 * 2048, r);
           mma_bf16(o[jd], h0, l0, h1, l1, r[0], r[1]);
           mma_bf16(o[jd + 1], h0, l0, h1, l1, r[2], r[3]);
+          if (fine) {
+            mma_bf16(o[jd], e0, 0u, e1, 0u, r[0], r[1]);
+            mma_bf16(o[jd + 1], e0, 0u, e1, 0u, r[2], r[3]);
+          }
         }
       }
     }

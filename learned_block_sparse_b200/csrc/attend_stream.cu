@@ -6,7 +6,9 @@
 // product is a butterfly over those lanes, the products with V need none. A warp has
 // kLoads loads of K and of V in flight (8 KB), twelve or more warps share an SM.
 // Groups of lanes, warps and thread blocks each keep their own running maximum, sum
-// and output, added at the end in a fixed order.
+// and output, added at the end in a fixed order. Measured: the gated fp32 window, 15.3 us
+// with the merge's launch against 4.6 of bytes; latency (loads 4.4 of every 11 stalled
+// cycles) and two launches, not bandwidth, at this size.
 #include "attend_common.cuh"
 
 namespace eta {

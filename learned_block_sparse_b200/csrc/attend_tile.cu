@@ -18,9 +18,16 @@
 // such maximum, so they stay below 2^8), which after the first tiles is rare.
 //
 // Rounding: the weights meet V as bf16 numbers. With bf16 output that one rounding
-// (half a step, 2^-9 of each weight, signs random) is of the output's own size; with
-// fp32 output a second MMA adds the weights' remainders, also as bf16 numbers, so 16
-// bits of every weight take part. Sums, maxima and accumulators are fp32.
+// (half a step, 2^-9 of each weight, signs random) is of the output's own size. With
+// fp32 output (FINE) a weight is the sum of three bf16 numbers, 24 bits, in three MMAs;
+// their columns take the second tile's S, so a block then holds one tile. Sums, maxima
+// and accumulators are fp32. The tensor cores' additions to an accumulator cut off
+// instead of rounding, so its error grows with their number in one direction; FINE
+// therefore starts a new accumulator every kFlush key tiles and adds the old one to a
+// second with rounded fp32 additions (at so + D). (Two tiles, 16 bits per weight, one
+// accumulator: an error of 2.6e-5 behind 32K unsplit keys where this has 1.9e-6; 234 us
+// where this takes 436 with 8 rows of 64 tokens and 16 KV heads of 64; the same time
+// within windows of 1.8K keys, 51 us.)
 //
 // Keys that no query of the tile sees (past the row's end, before the window, a
 // page outside the pool) may hold anything in memory. Their logits are replaced by
@@ -29,8 +36,12 @@
 //
 // Bound: the matrix pipe and the exponentials are balanced on this machine (a
 // 128 x 128 x 128 pair of MMAs takes 1,024 cycles, its 16,384 exponentials 1,024
-// cycles of the special-function units); long prefixes with few rows are bound by
-// HBM.
+// cycles of the special-function units), and each is busy half of the time: what is
+// left is the chain of a key tile (wait for S, TMEM load, maximum, weights: ~3,900
+// cycles for the two query tiles). Measured: 821 TFLOP/s (0.51 of the matrix rate)
+// for chunks behind a window of 4,096, 243 us; gates add one exponential and a
+// reciprocal per logit, and the special-function units are busy 73% (128K prefix, 32
+// tokens, 32 / 4 heads of 64: 142 us).
 //
 // fp8 (e4m3) caches: the tiles arrive as bytes and six warps widen them to bf16,
 // exactly, into the ring the MMAs read. (f16 would take a third of the conversions, but
@@ -53,6 +64,7 @@ constexpr int kConvWarps = 6;         // of them widening
 constexpr int kTR = 128;  // rows per query tile
 constexpr int kTK = 128;  // keys per key tile
 constexpr int kHK = 64;   // keys per half of it: a step of the softmax
+constexpr int kFlush = 4;  // key tiles per accumulator with fp32 output
 
 enum { kNoGate = 0, kSigmoid = 1, kHard = 2 };
 
@@ -151,7 +163,7 @@ struct TileSmem {
   static constexpr int kBytes = 2 * kQ + kBufs * kTile + kRawBufs * kRaw + 512;  // barriers and flags at the end
 };
 
-template <int D, int GATE, bool HILO, bool FP8>
+template <int D, int GATE, bool FINE, bool FP8>
 __global__ void __launch_bounds__(FP8 ? kTileThreadsFp8 : kTileThreads, 1)
     attend_tile_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap tmq,
                        const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const int prefix, const int box_rows,
@@ -202,7 +214,7 @@ __global__ void __launch_bounds__(FP8 ? kTileThreadsFp8 : kTileThreads, 1)
   const int G = a.G;
   int g_log2 = 0;
   while ((1 << g_log2) < G) ++g_log2;
-  const int qt_log2 = 8 - g_log2;  // 256 rows
+  const int qt_log2 = (FINE ? 7 : 8) - g_log2;  // 128 or 256 rows
   OwnTile t;
   Visible vis;
   int tiles, tiles_a = 0;
@@ -218,7 +230,7 @@ __global__ void __launch_bounds__(FP8 ? kTileThreadsFp8 : kTileThreads, 1)
   } else {
     if (a.longest_first) {
       // Longest tiles first, all their heads together: with ~4 tiles per SM the last
-      // ones decide (chunks of 8 rows, window 4096: 280 -> 253 us). Thread i counts tile i's keys.
+      // ones decide (chunks of 8 rows, window 4096: 280 -> 253 us, of 243 now). Thread i counts tile i's keys.
       uint32_t* keys = reinterpret_cast<uint32_t*>(tile_smem);
       const int order = (blockIdx.y * gridDim.x + blockIdx.x) / gridDim.y;
       h = (blockIdx.y * gridDim.x + blockIdx.x) % gridDim.y;
@@ -294,7 +306,7 @@ __global__ void __launch_bounds__(FP8 ? kTileThreadsFp8 : kTileThreads, 1)
 #pragma unroll
           for (int x = 0; x < D / 64; ++x)
             tma_load_box3(s_q + w * L::kQ + x * kTR * 128, &tmq, x * 64, h * G,
-                          static_cast<int>(t.tok0) + (w << (qt_log2 - 1)), s_qrdy);
+                          static_cast<int>(t.tok0) + (w << (7 - g_log2)), s_qrdy);
       }
       __syncwarp();
       for (int j = 0; j < n; ++j) {
@@ -344,7 +356,7 @@ __global__ void __launch_bounds__(FP8 ? kTileThreadsFp8 : kTileThreads, 1)
       // ------------------------------------------------------------------ MMAs
       // The whole warp runs this, every value uniform; one lane issues (see elect_lane).
       // TMEM is allocated whole, so its columns are compile-time constants: S of tile w
-      // at 128 w (P over it: 64 columns, the remainders in the next 64), O at 256 + D w.
+      // at 128 w (P over it: 64 columns; FINE: the further parts in the next 128), O at 256 + D w.
       constexpr uint32_t dS = mma_desc_bf16(kTR, kTK, false), dO = mma_desc_bf16(kTR, D, true);
       const uint32_t q_lo = desc_lo(smem_u32(s_q), 16);
       const uint32_t k_lo = desc_lo(smem_u32(s_kv), 16), v_lo = desc_lo(smem_u32(s_kv), kTK * 128);
@@ -389,14 +401,15 @@ __global__ void __launch_bounds__(FP8 ? kTileThreadsFp8 : kTileThreads, 1)
             if (elect_lane()) {
               const uint32_t v = v_lo + vb * (L::kTile >> 4) + half * (kHK * 128 >> 4);
               const uint32_t o = 256 + w * D, p = w * 128 + half * (kHK / 2);
-              const uint32_t first = j == 0 && half == 0 ? 0u : 1u;
+              const uint32_t first = (FINE ? j % kFlush : j) == 0 && half == 0 ? 0u : 1u;
 #pragma unroll
               for (int ks = 0; ks < kHK / 16; ++ks)
                 mma_f16_ts(o, p + ks * 8, desc_of(v + ks * (2048 >> 4)), dO, ks == 0 ? first : 1u);
-              if (HILO) {
+              if (FINE) {
 #pragma unroll
-                for (int ks = 0; ks < kHK / 16; ++ks)
-                  mma_f16_ts(o, p + 64 + ks * 8, desc_of(v + ks * (2048 >> 4)), dO, 1u);
+                for (int ks = 0; ks < kHK / 8; ++ks)  // the second parts, then the third
+                  mma_f16_ts(o, p + 64 * (1 + ks / (kHK / 16)) + ks % (kHK / 16) * 8,
+                             desc_of(v + ks % (kHK / 16) * (2048 >> 4)), dO, 1u);
               }
             }
             __syncwarp();
@@ -564,20 +577,32 @@ __global__ void __launch_bounds__(FP8 ? kTileThreadsFp8 : kTileThreads, 1)
       float mx = fmaxf(max3(m0, m1, m2), m3);
       if (GATE == kNoGate) mx *= c2;
       const bool grow = mx > m + 8.0f;  // (also the first visible key: m is -inf until then)
-      if (__any_sync(kFull, grow)) {
+      const bool flush = FINE && j > 0 && j % kFlush == 0;
+      if (__any_sync(kFull, grow) || flush) {
         const float mn = grow ? mx : m;
         const float f = m == mn ? 1.0f : ex2(m - mn);
         l *= f;
         m = mn;
         if (j > 0) {  // (the MMAs of the last key tile are done: the barrier that released S follows them)
-#pragma unroll
+#pragma unroll(FINE ? 1 : D / 32)
           for (int k = 0; k < D / 32; ++k) {
             float o[32];
             tmem_ld32(so + 32 * k, reinterpret_cast<uint32_t*>(o));
             tc_wait_ld();
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] *= f;
-            tmem_st32(so + 32 * k, reinterpret_cast<const uint32_t*>(o));
+            if (FINE && j > kFlush) {  // the sum of the flushed tiles
+              float o2[32];
+              tmem_ld32(so + D + 32 * k, reinterpret_cast<uint32_t*>(o2));
+              tc_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                o2[e] *= f;
+                o[e] += flush ? o2[e] : 0.0f;
+              }
+              if (!flush) tmem_st32(so + D + 32 * k, reinterpret_cast<const uint32_t*>(o2));
+            }
+            tmem_st32((flush ? so + D : so) + 32 * k, reinterpret_cast<const uint32_t*>(o));
           }
         }
       }
@@ -588,25 +613,36 @@ __global__ void __launch_bounds__(FP8 ? kTileThreadsFp8 : kTileThreads, 1)
       uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        uint32_t hi[32], lo[HILO ? 32 : 1];
+        uint32_t part[32];
 #pragma unroll
         for (int k = 0; k < 32; k += 2) {
-          const float* e = s + half * kHK + 2 * k;
+          float* e = s + half * kHK + 2 * k;
           const uint64_t y0 = fma2(pair(e[0], e[1]), scale2, base2);
           const uint64_t y1 = fma2(pair(e[2], e[3]), scale2, base2);
           const float2 z0 = unpair(y0), z1 = unpair(y1);
           const float x0 = ex2(z0.x), x1 = ex2(z0.y), x2 = ex2(z1.x), x3 = ex2(z1.y);
           sum0 = add2(sum0, pair(x0, x1));
           sum1 = add2(sum1, pair(x2, x3));
-          hi[k] = pack2(x0, x1);
-          hi[k + 1] = pack2(x2, x3);
-          if (HILO) {
-            lo[k] = pack2(x0 - bf16_lo(hi[k]), x1 - bf16_hi(hi[k]));
-            lo[k + 1] = pack2(x2 - bf16_lo(hi[k + 1]), x3 - bf16_hi(hi[k + 1]));
+          part[k] = pack2(x0, x1);
+          part[k + 1] = pack2(x2, x3);
+          if (FINE) {
+            e[0] = x0, e[1] = x1, e[2] = x2, e[3] = x3;
           }
         }
-        tmem_st32(sp + half * 32, hi);
-        if (HILO) tmem_st32(sp + 64 + half * 32, lo);
+        tmem_st32(sp + half * 32, part);
+        if (FINE) {
+#pragma unroll 1
+          for (int further = 1; further <= 2; ++further) {  // what the parts before leave
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              float* e = s + half * kHK + 2 * k;
+              e[0] -= bf16_lo(part[k]);
+              e[1] -= bf16_hi(part[k]);
+              part[k] = pack2(e[0], e[1]);
+            }
+            tmem_st32(sp + 64 * further + half * 32, part);
+          }
+        }
         tc_wait_st();
         tc_fence_before();
         mbar_arrive(&s_prdy[2 * w + half]);
@@ -627,21 +663,39 @@ __global__ void __launch_bounds__(FP8 ? kTileThreadsFp8 : kTileThreads, 1)
       const bool narrow = direct && a.out_dtype == ETA_BF16;
       if (n > 0) {
         unsigned char* mine = s_q + (w * kTR + r) * (D * 4 + 16);
-        float o[D];
+        if (FINE) {
+#pragma unroll 1
+          for (int k = 0; k < D / 32; ++k) {
+            float o[32], o2[32];
+            tmem_ld32(so + 32 * k, reinterpret_cast<uint32_t*>(o));
+            if (n > kFlush) tmem_ld32(so + D + 32 * k, reinterpret_cast<uint32_t*>(o2));
+            tc_wait_ld();
+            if (n > kFlush) {
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k) tmem_ld32(so + 32 * k, reinterpret_cast<uint32_t*>(o) + 32 * k);
-        tc_wait_ld();
-        if (narrow) {
+              for (int e = 0; e < 32; ++e) o[e] += o2[e];
+            }
 #pragma unroll
-          for (int e = 0; e < D; e += 8)
-            *reinterpret_cast<uint4*>(mine + 2 * e) =
-                make_uint4(pack2(o[e] * inv, o[e + 1] * inv), pack2(o[e + 2] * inv, o[e + 3] * inv),
-                           pack2(o[e + 4] * inv, o[e + 5] * inv), pack2(o[e + 6] * inv, o[e + 7] * inv));
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<float4*>(mine + 4 * (32 * k + e)) =
+                  make_float4(o[e] * inv, o[e + 1] * inv, o[e + 2] * inv, o[e + 3] * inv);
+          }
         } else {
+          float o[D];
 #pragma unroll
-          for (int e = 0; e < D; e += 4)
-            *reinterpret_cast<float4*>(mine + 4 * e) =
-                make_float4(o[e] * inv, o[e + 1] * inv, o[e + 2] * inv, o[e + 3] * inv);
+          for (int k = 0; k < D / 32; ++k) tmem_ld32(so + 32 * k, reinterpret_cast<uint32_t*>(o) + 32 * k);
+          tc_wait_ld();
+          if (narrow) {
+#pragma unroll
+            for (int e = 0; e < D; e += 8)
+              *reinterpret_cast<uint4*>(mine + 2 * e) =
+                  make_uint4(pack2(o[e] * inv, o[e + 1] * inv), pack2(o[e + 2] * inv, o[e + 3] * inv),
+                             pack2(o[e + 4] * inv, o[e + 5] * inv), pack2(o[e + 6] * inv, o[e + 7] * inv));
+          } else {
+#pragma unroll
+            for (int e = 0; e < D; e += 4)
+              *reinterpret_cast<float4*>(mine + 4 * e) =
+                  make_float4(o[e] * inv, o[e + 1] * inv, o[e + 2] * inv, o[e + 3] * inv);
+          }
         }
         fence_async_smem();
         if (live) {
@@ -676,12 +730,12 @@ __global__ void __launch_bounds__(FP8 ? kTileThreadsFp8 : kTileThreads, 1)
   end_pass(a, prefix != 0);
 }
 
-template <int D, int GATE, bool HILO, bool FP8>
+template <int D, int GATE, bool FINE, bool FP8>
 cudaError_t launch_tile_t(const AttendArgs& a, dim3 grid, bool prefix, const CUtensorMap& tmq, const CUtensorMap& tmk,
                           const CUtensorMap& tmv,
                           int box_rows, int store_rows, cudaStream_t st) {
   static std::atomic<uint64_t> smem_done{0};
-  cudaError_t e = allow_max_smem(smem_done, reinterpret_cast<const void*>(attend_tile_kernel<D, GATE, HILO, FP8>));
+  cudaError_t e = allow_max_smem(smem_done, reinterpret_cast<const void*>(attend_tile_kernel<D, GATE, FINE, FP8>));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
@@ -691,7 +745,7 @@ cudaError_t launch_tile_t(const AttendArgs& a, dim3 grid, bool prefix, const CUt
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, attend_tile_kernel<D, GATE, HILO, FP8>, a, tmq, tmk, tmv, prefix ? 1 : 0, box_rows, store_rows);
+  e = cudaLaunchKernelEx(&cfg, attend_tile_kernel<D, GATE, FINE, FP8>, a, tmq, tmk, tmv, prefix ? 1 : 0, box_rows, store_rows);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -721,7 +775,7 @@ cudaError_t launch_attend_tile(const AttendArgs& a, int kv_dtype, int D, bool pr
       !encode_rows_map(&tmv, prefix ? a.pv : a.v, store, D, fp8 ? 1 : 2, box_rows))
     return cudaErrorInvalidValue;
   AttendArgs args = a;
-  const int64_t qt = kTileRows / a.G;
+  const int64_t qt = tile_rows(a.out_dtype) / a.G;
   const int64_t items = prefix ? (a.T + qt - 1) / qt : (a.cu_q != nullptr ? a.T / qt + a.B : a.B);
   args.longest_first = !prefix && items * a.Hkv > device_sm_count() && items <= (fp8 ? kTileThreadsFp8 : kTileThreads);
   const dim3 grid(static_cast<unsigned>(items), static_cast<unsigned>(a.Hkv),

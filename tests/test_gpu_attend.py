@@ -432,3 +432,33 @@ def test_calls_that_cannot_be_right_are_refused():
             print("accepted", i)
     torch.cuda.synchronize()
     assert dec.device_status() == 0
+
+
+@pytest.mark.parametrize("kv,Hkv,d", [("bf16", 4, 64), ("bf16", 2, 128), ("fp8", 2, 128)])
+def test_long_sums_keep_fp32(kv, Hkv, d):
+    """Values of one sign behind a long prefix that is not split: an accumulator that
+    cuts off each addition would drift with their number (4,096 additions of half a step
+    of 2^-23 and more are 2e-4). Counted here: 96 additions of at most 2^-23 between two
+    rounded sums (64 of 2^-24), and 2^-22 of each weight for its exponent: 1.6e-5."""
+    P, T, Hq = 32768, 12800 // Hkv, 2 * Hkv
+    g = torch.Generator(device="cuda").manual_seed(9)
+
+    def normal(*shape):
+        return torch.empty(shape, device="cuda").normal_(0, 1, generator=g)
+
+    pk, pv = (0.3 * normal(Hkv, P, d)).to(KV[kv]), (1 + normal(Hkv, P, d).abs()).to(KV[kv])
+    k, v = (0.3 * normal(1, Hkv, T, d)).to(KV[kv]), (1 + normal(1, Hkv, T, d).abs()).to(KV[kv])
+    q = normal(T, Hq, d).to(torch.bfloat16)
+    dec = binding.EtaDecoder(1, Hq, Hkv, d, 32, T, kv_dtype=KV[kv], q_dtype=torch.bfloat16)
+    out = torch.empty((T, Hq, d), device="cuda")
+    dec.shared(q, k, v, T, binding.Prefix(P, k=pk, v=pv), out=out,
+               cu_q=torch.tensor([0, T], dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    assert dec.device_status() == 0
+    for t in (0, 1, 129, T // 2, T - 1):
+        for h in range(Hq):
+            keys = torch.cat([pk[h // 2].float(), k[0, h // 2, :t + 1].float()]).double()
+            vals = torch.cat([pv[h // 2].float(), v[0, h // 2, :t + 1].float()]).double()
+            w = torch.softmax(keys @ q[t, h].double() / d ** 0.5, 0)
+            exact = w @ vals
+            assert ((out[t, h].double() - exact).abs() / exact).max() < 1.6e-5, (t, h)
