@@ -205,6 +205,9 @@ def make_shape(batch, n_q_heads, n_kv_heads, head_dim, block_size, capacity, kv_
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
+_capturing = torch.cuda.is_current_stream_capturing
+
+
 def _current(index: int) -> bool:
     """Whether CUDA device `index` is the current one."""
     return index == torch.cuda.current_device()
@@ -496,6 +499,7 @@ class EtaDecoder:
         self.out = torch.empty((batch, n_q_heads, head_dim), **f)
         self.kv_dtype, self.q_dtype = _DTYPES[self.shape.kv_dtype], _DTYPES[self.shape.q_dtype]
         self.attend_ws, self._reserved = None, -1  # see reserve_queries
+        self._in_graph, self._graph_ws = False, []  # workspaces that captured graphs still write to
         self._geometry = (batch, n_q_heads, n_kv_heads, head_dim, block_size, capacity)
         self._cache_shape = (batch, n_kv_heads, capacity, head_dim)
         self._refs = (ctypes.byref(self.shape), ctypes.byref(self.meta_shape), ctypes.byref(self.params))
@@ -641,7 +645,10 @@ class EtaDecoder:
     def reserve_queries(self, n: int) -> None:
         """Workspace of :meth:`window` and :meth:`shared` for calls of up to ``n`` new
         tokens. A larger call reserves for itself, which allocates: reserve the
-        largest before capturing a CUDA graph."""
+        largest before capturing a CUDA graph. A workspace that captured calls use
+        lives as long as the decoder, so a later, larger call leaves those graphs
+        valid. Calls (and replays) of one decoder follow one another: two streams at
+        once take two decoders."""
         if n <= self._reserved:
             return
         with torch.cuda.device(self.mu.device):
@@ -654,6 +661,11 @@ class EtaDecoder:
             off = (-ws.data_ptr()) % 256
             ws = ws[off:off + need]
             _check(lib.eta_workspace_init(_ptr(ws), need, _stream()), "eta_workspace_init")
+            if self._in_graph:  # captured calls hold the old one's address
+                self._graph_ws.append(self.attend_ws)
+                self._in_graph = False
+            elif self.attend_ws is not None:
+                self.attend_ws.record_stream(torch.cuda.current_stream())
             self.attend_ws, self._reserved = ws, n
 
     def _query_args(self, q, tau, tau_batch_stride, cu_q, out, dev, what):
@@ -703,6 +715,8 @@ class EtaDecoder:
         queries, out, n = self._query_args(q, tau, tau_batch_stride, cu_q, out, dev, "window")
         if n > self._reserved:
             self.reserve_queries(n)
+        if _capturing():
+            self._in_graph = True
         status = lib.eta_attend_window(self._refs[0], self._refs[2], queries, k.data_ptr(), v.data_ptr(), pages,
                                        None if seq_lens is None else seq_lens.data_ptr(), n_tokens, window, sinks,
                                        self.attend_ws.data_ptr(), self.attend_ws.numel(), _raw_stream(dev))
@@ -736,6 +750,8 @@ class EtaDecoder:
                 raise ValueError("shared: prefix blocks cover n_tokens, beside K")
         if n > self._reserved:
             self.reserve_queries(n)
+        if _capturing():
+            self._in_graph = True
         status = lib.eta_attend_shared(self._refs[0], self._refs[2], queries, ctypes.byref(prefix.args), k.data_ptr(),
                                        v.data_ptr(), pages, None if seq_lens is None else seq_lens.data_ptr(),
                                        n_tokens, self.attend_ws.data_ptr(), self.attend_ws.numel(), _raw_stream(dev))
@@ -746,6 +762,7 @@ class EtaDecoder:
     def device_status(self) -> int:
         """Status of this decoder's calls since the last read, and clears it."""
         status = read_device_status(self.ws)
-        if self.attend_ws is not None:
-            status = read_device_status(self.attend_ws) or status
+        for ws in (*self._graph_ws, self.attend_ws):
+            if ws is not None:
+                status = read_device_status(ws) or status
         return status

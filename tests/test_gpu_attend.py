@@ -462,3 +462,29 @@ def test_long_sums_keep_fp32(kv, Hkv, d):
             w = torch.softmax(keys @ q[t, h].double() / d ** 0.5, 0)
             exact = w @ vals
             assert ((out[t, h].double() - exact).abs() / exact).max() < 1.6e-5, (t, h)
+
+
+def test_a_larger_call_leaves_captured_graphs_valid():
+    """A captured call, then a larger one that takes a larger workspace: the graph's own stays."""
+    c = Case(rows=((1, 500), (1, 90)), seed=6)
+    p = make(c, prefix=300)
+    dec = decoder(c)
+    out = torch.full((c.T, c.Hq, c.d), FILL, device="cuda")
+    dec.shared(p["q"], p["K"], p["V"], c.cap, p["prefix"], seq_lens=p["lens"], out=out)
+    first = out.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dec.shared(p["q"], p["K"], p["V"], c.cap, p["prefix"], seq_lens=p["lens"], out=out)
+    ws = dec.attend_ws
+    address, size = ws.data_ptr(), ws.numel()
+    del ws
+    dec.reserve_queries(5000)
+    assert dec.attend_ws.data_ptr() != address
+    other = [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    assert all(x.data_ptr() + size <= address or x.data_ptr() >= address + size for x in other)
+    out.fill_(FILL)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, first) and all(bool((x == 255).all()) for x in other)
+    assert dec.device_status() == 0
+    check(p, out, reference(p, prefix=True), FILL)
