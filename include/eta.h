@@ -503,8 +503,8 @@ ETA_API eta_status_t eta_append_kv(const eta_shape_t* shape, const eta_tokens_t*
 /* Packed queries q [n_new][Hq][d] (q_dtype), cu_q as above; thresholds of token t
  * and head h at tau[t * tau_stride + h] (0: per-head constants), or tau == NULL for
  * plain softmax attention; out [n_new][Hq][d] in out_dtype (ETA_F32 or ETA_BF16),
- * 16-byte aligned like q. The gate is params->gate with params->beta, the query's
- * own token exempt. Nothing else of params is read. */
+ * 16-byte aligned like q and apart from it. The gate is params->gate with
+ * params->beta, the query's own token exempt. Nothing else of params is read. */
 typedef struct {
   const void* q;
   const int32_t* cu_q;

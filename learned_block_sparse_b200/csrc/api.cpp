@@ -311,6 +311,12 @@ eta_status_t check_token_rows(const void* p, int64_t stride, int64_t row, int64_
   return stride >= row && (stride * elem) % 16 == 0 ? ETA_OK : ETA_ERR_INVALID_ARG;
 }
 
+// Whether `out_bytes` bytes written at `out` reach into `n` rows of `row` bytes, `stride` bytes apart.
+bool overlaps(const void* out, int64_t out_bytes, const void* in, int64_t n, int64_t stride, int64_t row) {
+  const uintptr_t o = reinterpret_cast<uintptr_t>(out), i = reinterpret_cast<uintptr_t>(in);
+  return n > 0 && o < i + static_cast<uintptr_t>((n - 1) * stride + row) && i < o + static_cast<uintptr_t>(out_bytes);
+}
+
 // The checks and fields that the attention calls of new tokens share.
 eta_status_t make_attend(const eta_shape_t* s, const eta_params_t* p, const eta_queries_t* in, const void* k,
                          const void* v, const eta_pages_t* pages, const int32_t* seq_lens, int64_t n, void* ws,
@@ -330,6 +336,8 @@ eta_status_t make_attend(const eta_shape_t* s, const eta_params_t* p, const eta_
   if (static_cast<int64_t>(s->batch) * s->n_kv_heads > kMaxBH) return ETA_ERR_UNSUPPORTED;
   // token x head rows, and positions up to a tile past a row's end, are 32-bit integers in the kernels
   if (in->n_new * s->n_q_heads > INT32_MAX || s->capacity > INT32_MAX - kPositionSlack) return ETA_ERR_UNSUPPORTED;
+  const int64_t values = in->n_new * s->n_q_heads * s->head_dim, q_bytes = values * elem_bytes(s->q_dtype);
+  if (overlaps(in->out, values * elem_bytes(in->out_dtype), in->q, 1, 0, q_bytes)) return ETA_ERR_INVALID_ARG;
   if (ws == nullptr || !aligned(ws, 256) || ws_bytes < attend_workspace_bytes(*s, in->n_new, with_prefix))
     return ETA_ERR_WORKSPACE;
   std::memset(c, 0, sizeof(*c));
@@ -689,6 +697,11 @@ ETA_API eta_status_t eta_append_kv(const eta_shape_t* shape, const eta_tokens_t*
   if (tokens->q != nullptr) {
     ETA_TRY(check_token_rows(tokens->q, tokens->q_stride, shape->n_q_heads * d, e));
     if (!aligned(tokens->q_out, 16)) return ETA_ERR_INVALID_ARG;
+    const int64_t n = tokens->n_new, q_row = shape->n_q_heads * d * e, kv_row = shape->n_kv_heads * d * e;
+    if (overlaps(tokens->q_out, n * q_row, tokens->q, n, tokens->q_stride * e, q_row) ||
+        overlaps(tokens->q_out, n * q_row, tokens->k, n, tokens->k_stride * e, kv_row) ||
+        overlaps(tokens->q_out, n * q_row, tokens->v, n, tokens->v_stride * e, kv_row))
+      return ETA_ERR_INVALID_ARG;
   }
   if (rope->rot_dim < 0 || rope->rot_dim > shape->head_dim || rope->rot_dim % 16 != 0) return ETA_ERR_INVALID_ARG;
   if (rope->interleaved != 0 && rope->interleaved != 1) return ETA_ERR_INVALID_ARG;

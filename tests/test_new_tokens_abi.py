@@ -8,6 +8,7 @@ import pytest
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 A = 1 << 20        # an aligned address; no call here gets as far as using it
+OUT = A + (1 << 24)
 
 
 def _b():
@@ -23,7 +24,7 @@ def _shape(**kw):
 
 def _append(shape=None, tokens=None, rope=None, k=A, v=A, pages=None, lens=A, n=1024, meta=None, ws=A, ws_bytes=1 << 20):
     b = _b()
-    t = dict(q=A, k=A, v=A, q_out=A, q_stride=512, k_stride=256, v_stride=256, cu_new=A, n_new=7)
+    t = dict(q=A, k=A, v=A, q_out=OUT, q_stride=512, k_stride=256, v_stride=256, cu_new=A, n_new=7)
     t.update(tokens or {})
     r = dict(inv_freq=A, rot_dim=128, interleaved=0)
     r.update(rope or {})
@@ -41,6 +42,8 @@ def _append(shape=None, tokens=None, rope=None, k=A, v=A, pages=None, lens=A, n=
     (dict(tokens=dict(k=None)), 1), (dict(tokens=dict(v=A + 8)), 1), (dict(tokens=dict(q=A + 4)), 1),
     (dict(tokens=dict(q=None)), 1), (dict(tokens=dict(q_out=None)), 1), (dict(tokens=dict(q_out=A + 4)), 1),
     (dict(tokens=dict(k_stride=255)), 1), (dict(tokens=dict(k_stride=260)), 1), (dict(tokens=dict(q_stride=256)), 1),
+    (dict(tokens=dict(q_out=A)), 1), (dict(tokens=dict(q_out=A + 7 * 1024 - 16)), 1),  # q_out reaches into q
+    (dict(tokens=dict(q_out=A, q=OUT)), 1), (dict(tokens=dict(q_out=A - 16)), 1),      # into k and v; into q from before
     (dict(rope=dict(rot_dim=-16)), 1), (dict(rope=dict(rot_dim=144)), 1), (dict(rope=dict(rot_dim=40)), 1),
     (dict(rope=dict(inv_freq=None)), 1), (dict(rope=dict(inv_freq=A + 2)), 1), (dict(rope=dict(interleaved=2)), 1),
     (dict(k=None), 1), (dict(v=A + 8), 1), (dict(lens=A + 1), 1), (dict(n=0), 1), (dict(n=1025), 1),
@@ -63,7 +66,7 @@ def test_append_refuses_shapes_and_pages():
 def _attend(call="window", shape=None, params=None, queries=None, prefix=None, k=A, v=A, pages=None, lens=A, n=1024,
             window=64, sinks=4, ws=A, ws_bytes=1 << 40):
     b = _b()
-    q = dict(q=A, cu_q=A, n_new=7, tau=None, tau_stride=0, out=A, out_dtype=1)
+    q = dict(q=A, cu_q=A, n_new=7, tau=None, tau_stride=0, out=OUT, out_dtype=1)
     q.update(queries or {})
     s, p, qs = shape or _shape(), params or b.make_params(), b.Queries(**q)
     pg = ctypes.byref(pages) if pages is not None else None
@@ -82,6 +85,8 @@ COMMON = [
     (dict(queries=dict(n_new=-1)), 1), (dict(queries=dict(cu_q=None, n_new=3)), 1), (dict(queries=dict(cu_q=A + 1)), 1),
     (dict(queries=dict(q=None)), 1), (dict(queries=dict(q=A + 8)), 1), (dict(queries=dict(out=None)), 1),
     (dict(queries=dict(out=A + 4)), 1), (dict(queries=dict(out_dtype=2)), 1),
+    (dict(queries=dict(out=A)), 1), (dict(queries=dict(out=A + 7 * 1024 - 16)), 1),    # out reaches into q
+    (dict(queries=dict(out=A - 16)), 1),
     (dict(queries=dict(tau=A, tau_stride=-1)), 1), (dict(queries=dict(tau=A + 2)), 1),
     (dict(queries=dict(n_new=(1 << 31) - 1)), 2),                     # token x head rows past 32 bits
     (dict(k=None), 1), (dict(v=A + 8), 1), (dict(lens=A + 2), 1), (dict(n=0), 1), (dict(n=1025), 1),
