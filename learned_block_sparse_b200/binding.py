@@ -203,9 +203,7 @@ def make_shape(batch, n_q_heads, n_kv_heads, head_dim, block_size, capacity, kv_
 # The calls for new tokens are a few microseconds of GPU work in a decode step, so
 # their host side counts: raw stream handles and pointers as plain integers.
 _raw_stream = torch._C._cuda_getCurrentRawStream
-
-
-_capturing = torch.cuda.is_current_stream_capturing
+_capturing = torch._C._cuda_isCurrentStreamCapturing
 
 
 def _current(index: int) -> bool:
